@@ -6,9 +6,10 @@ library's kernels.  There is no fallback: if the library cannot be loaded, every
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -30,6 +31,9 @@ UNSTEP_ERR_DEVICE_BOUNDS = -10
 UNSTEP_APPEND_DEFER_Q_ROPE = 1   # unstep_rope_kv_append_ex: leave q alone
 UNSTEP_ATTN_ROPE_Q = 1           # unstep_window_attn_ex: q is un-rotated, rotate it in-kernel
 
+UNSTEP_BF16, UNSTEP_F32 = 0, 1                   # element types
+UNSTEP_NORM_LAYER, UNSTEP_NORM_RMS = 0, 1        # unstep_norm_t.kind
+
 
 class unstep_cache_t(ctypes.Structure):
     _fields_ = [
@@ -48,6 +52,18 @@ class unstep_cache_t(ctypes.Structure):
         ("act_B", ctypes.c_int), ("act_H", ctypes.c_int),
         ("b0", ctypes.c_int), ("h0", ctypes.c_int),
     ]
+
+
+class unstep_q8_cache_t(ctypes.Structure):
+    _fields_ = [("base", unstep_cache_t), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
+class unstep_norm_t(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int), ("eps", ctypes.c_float), ("param_type", ctypes.c_int),
+                ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("shift", ctypes.c_void_p),
+                ("mod_stride", ctypes.c_longlong)]
 
 
 class unstep_grid_t(ctypes.Structure):
@@ -103,6 +119,32 @@ _SIGNATURES = {
                            ctypes.c_void_p], ctypes.c_int),
     "unstep_cache_restore": ([ctypes.POINTER(unstep_cache_t), ctypes.c_void_p, ctypes.c_size_t,
                               ctypes.c_void_p], ctypes.c_int),
+    "unstep_q8_cache_kv_bytes": ([ctypes.POINTER(unstep_q8_cache_t)], ctypes.c_size_t),
+    "unstep_q8_cache_scale_bytes": ([ctypes.POINTER(unstep_q8_cache_t)], ctypes.c_size_t),
+    "unstep_q8_cache_init": ([ctypes.POINTER(unstep_q8_cache_t), ctypes.c_void_p], ctypes.c_int),
+    "unstep_q8_rope_kv_append": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                  ctypes.c_void_p, ctypes.POINTER(unstep_q8_cache_t),
+                                  ctypes.c_int, unstep_grid_t, ctypes.c_void_p], ctypes.c_int),
+    "unstep_q8_window_attn": ([ctypes.c_void_p, ctypes.POINTER(unstep_q8_cache_t), ctypes.c_int,
+                               ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
+    "unstep_q8_cache_read": ([ctypes.POINTER(unstep_q8_cache_t), ctypes.c_int, ctypes.c_int,
+                              ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
+    "unstep_q8_cache_state_bytes": ([ctypes.POINTER(unstep_q8_cache_t)], ctypes.c_size_t),
+    "unstep_q8_cache_save": ([ctypes.POINTER(unstep_q8_cache_t), ctypes.c_void_p,
+                              ctypes.c_size_t, ctypes.c_void_p], ctypes.c_int),
+    "unstep_q8_cache_restore": ([ctypes.POINTER(unstep_q8_cache_t), ctypes.c_void_p,
+                                 ctypes.c_size_t, ctypes.c_void_p], ctypes.c_int),
+    "unstep_norm_modulate": ([ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_void_p,
+                              ctypes.c_longlong, ctypes.c_longlong, ctypes.c_int,
+                              ctypes.c_longlong, ctypes.POINTER(unstep_norm_t), ctypes.c_void_p],
+                             ctypes.c_int),
+    "unstep_gate_residual_norm": ([ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong,
+                                   ctypes.c_void_p, ctypes.c_longlong, ctypes.c_void_p,
+                                   ctypes.c_int, ctypes.c_longlong, ctypes.c_float,
+                                   ctypes.POINTER(unstep_norm_t), ctypes.POINTER(unstep_norm_t),
+                                   ctypes.c_void_p, ctypes.c_longlong, ctypes.c_void_p,
+                                   ctypes.c_longlong, ctypes.c_longlong, ctypes.c_int,
+                                   ctypes.c_longlong, ctypes.c_void_p], ctypes.c_int),
     "unstep_get_device_error": ([ctypes.POINTER(unstep_cache_t), ctypes.c_void_p], ctypes.c_int),
     "unstep_selftest_wait_timeout": ([ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p],
                                      ctypes.c_int),
@@ -181,7 +223,7 @@ class LayerCache:
         L = lib()
         dev = torch.device(device) if device is not None else torch.device("cuda",
                                                                            torch.cuda.current_device())
-        c = unstep_cache_t()
+        c = self.c = self._new_struct()
         c.B, c.H, c.D, c.Hg, c.Wg = B, H, D, Hg, Wg
         c.d_t, c.d_h, c.d_w, c.theta = d_t, d_h, d_w, float(theta)
         c.cap_frames, c.max_pos_t = cap_frames, max_pos_t
@@ -195,13 +237,10 @@ class LayerCache:
             raise UnstepError(UNSTEP_ERR_ARG, "cache shape rejected")
         self.Tf = Hg * Wg
         self.rows = cap_frames * self.Tf
-        self.k_cache = torch.empty((B, H, self.rows, D), dtype=torch.bfloat16, device=dev)
-        self.v_cache = torch.empty_like(self.k_cache)
+        self._alloc_rows(dev)
         self.slot_frame = torch.empty((cap_frames,), dtype=torch.int32, device=dev)
         self.cos_sin = torch.empty((tab_bytes // 4,), dtype=torch.float32, device=dev)
         self.dev_error = torch.zeros((1,), dtype=torch.int32, device=dev)
-        c.k_cache = self.k_cache.data_ptr()
-        c.v_cache = self.v_cache.data_ptr()
         c.slot_frame = self.slot_frame.data_ptr()
         c.cos_sin = self.cos_sin.data_ptr()
         c.dev_error = self.dev_error.data_ptr()
@@ -220,11 +259,19 @@ class LayerCache:
             self.scratch = scratch
             c.attn_scratch = scratch.data_ptr()
             c.attn_scratch_bytes = scratch.numel() * scratch.element_size()
-        self.c = c
         self.device = dev
-        with torch.cuda.device(dev):
-            _check(L.unstep_cache_init(ctypes.byref(c), _stream_handle(stream)),
-                   "unstep_cache_init")
+        self.reset(stream)
+
+    def _new_struct(self) -> unstep_cache_t:
+        return unstep_cache_t()
+
+    def _alloc_rows(self, dev: torch.device) -> None:
+        """Device memory of the K and V rows, and its pointers in the struct."""
+        c = self.c
+        self.k_cache = torch.empty((c.B, c.H, self.rows, c.D), dtype=torch.bfloat16, device=dev)
+        self.v_cache = torch.empty_like(self.k_cache)
+        c.k_cache = self.k_cache.data_ptr()
+        c.v_cache = self.v_cache.data_ptr()
 
     def reset(self, stream: Optional[torch.cuda.Stream] = None) -> None:
         """Back to an empty cache (zeroed K/V, no frames), as after construction."""
@@ -334,8 +381,7 @@ class LayerCache:
         buf = torch.empty((self.state_bytes(),), dtype=torch.uint8).pin_memory()
         s = stream if stream is not None else torch.cuda.current_stream(self.device)
         with torch.cuda.device(self.device):
-            _check(lib().unstep_cache_save(ctypes.byref(self.c), buf.data_ptr(), buf.numel(),
-                                           _stream_handle(s)), "unstep_cache_save")
+            self._save(buf.data_ptr(), buf.numel(), _stream_handle(s))
         s.synchronize()
         return buf
 
@@ -345,9 +391,15 @@ class LayerCache:
             raise ValueError("state must be a contiguous uint8 host tensor")
         s = stream if stream is not None else torch.cuda.current_stream(self.device)
         with torch.cuda.device(self.device):
-            _check(lib().unstep_cache_restore(ctypes.byref(self.c), buf.data_ptr(), buf.numel(),
-                                              _stream_handle(s)), "unstep_cache_restore")
+            self._restore(buf.data_ptr(), buf.numel(), _stream_handle(s))
         s.synchronize()     # the host buffer may be reused once the copies have run
+
+    def _save(self, ptr: int, n: int, handle: int) -> None:
+        _check(lib().unstep_cache_save(ctypes.byref(self.c), ptr, n, handle), "unstep_cache_save")
+
+    def _restore(self, ptr: int, n: int, handle: int) -> None:
+        _check(lib().unstep_cache_restore(ctypes.byref(self.c), ptr, n, handle),
+               "unstep_cache_restore")
 
     def device_error(self, stream: Optional[torch.cuda.Stream] = None) -> int:
         return lib().unstep_get_device_error(ctypes.byref(self.c), _stream_handle(stream))
@@ -372,6 +424,138 @@ class LayerCache:
             self.window_attn(bufs["q"], window, out=bufs["out"], stream=s, rope_q=rope_q_in_attn)
             out_h.copy_(bufs["out"], non_blocking=True)
         return out_h
+
+
+def _on(device: torch.device, stream: Optional[torch.cuda.Stream]):
+    """(stream handle on `device`, guard that makes `device` current for the call)."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    guard = _SAME_DEVICE if torch.cuda.current_device() == device.index else \
+        torch.cuda.device(device)
+    return int(s.cuda_stream), guard
+
+
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _new_on(stream: Optional[torch.cuda.Stream], shape, dtype, device) -> torch.Tensor:
+    """An output that a call on `stream` writes: its memory is not reused before the stream is
+    done with it."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+class LayerCacheQ8(LayerCache):
+    """A :class:`LayerCache` that holds K and V in one byte per element.
+
+    Every 32 channels of a row share a power-of-two scale and are held as e4m3 numbers, so the
+    cache takes 33/64 of the bf16 cache's memory.  ``k_codes`` and ``v_codes`` are
+    ``float8_e4m3fn [B][H][rows][D]``, ``k_scale`` and ``v_scale`` ``float8_e8m0fnu
+    [B][H][rows][D/32]``; an element's value is code times scale, exactly a bf16 number.  A block
+    of 32 channels in which a NaN or an infinity is written reads back as NaN.
+
+    Construction, frame order, windows, shards, scratch and checkpoints are LayerCache's; queries
+    are always rotated by the append (``defer_q`` and ``rope_q`` are not offered).
+    """
+
+    def _new_struct(self) -> unstep_cache_t:
+        self.q8 = unstep_q8_cache_t()
+        return self.q8.base
+
+    def _alloc_rows(self, dev: torch.device) -> None:
+        c = self.c
+        shape = (c.B, c.H, self.rows, c.D)
+        scales = (c.B, c.H, self.rows, c.D // 32)
+        self.k_codes = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
+        self.v_codes = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
+        self.k_scale = torch.empty(scales, dtype=torch.float8_e8m0fnu, device=dev)
+        self.v_scale = torch.empty(scales, dtype=torch.float8_e8m0fnu, device=dev)
+        c.k_cache, c.v_cache = self.k_codes.data_ptr(), self.v_codes.data_ptr()
+        self.q8.k_scale, self.q8.v_scale = self.k_scale.data_ptr(), self.v_scale.data_ptr()
+
+    def reset(self, stream: Optional[torch.cuda.Stream] = None) -> None:
+        """Back to an empty cache, as after construction."""
+        handle, guard = _on(self.device, stream)
+        with guard:
+            _check(lib().unstep_q8_cache_init(ctypes.byref(self.q8), handle),
+                   "unstep_q8_cache_init")
+
+    def rope_kv_append(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, frame_idx: int,
+                       frames: int, stream: Optional[torch.cuda.Stream] = None,
+                       defer_q: bool = False, q_out: Optional[torch.Tensor] = None
+                       ) -> torch.Tensor:
+        """Append rotated k and v as 8-bit rows; rotate q into ``q_out`` (None: in place).
+        Returns the rotated q."""
+        if defer_q:
+            raise ValueError("an 8-bit cache rotates the queries in the append (no defer_q)")
+        q_out = q if q_out is None else q_out
+        L = self.chunk_len(frames)
+        for t, n in ((q, "q"), (k, "k"), (v, "v"), (q_out, "q_out")):
+            self._check_act(t, L, n)
+        handle, guard = _on(self.device, stream)
+        with guard:
+            _check(lib().unstep_q8_rope_kv_append(
+                _dev_ptr(q, "q"), _dev_ptr(q_out, "q_out"), _dev_ptr(k, "k"), _dev_ptr(v, "v"),
+                ctypes.byref(self.q8), int(frame_idx),
+                unstep_grid_t(frames, self.c.Hg, self.c.Wg), handle), "unstep_q8_rope_kv_append")
+        return q_out
+
+    def window_attn(self, q: torch.Tensor, window: int, out: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None,
+                    rope_q: bool = False) -> torch.Tensor:
+        """Attention of the latest chunk's rotated queries over the last ``window`` frames."""
+        if rope_q:
+            raise ValueError("an 8-bit cache takes rotated queries (no rope_q)")
+        L = self.chunk_len(self.c.last_chunk_frames)
+        self._check_act(q, L, "q")
+        if out is None:
+            out = _new_on(stream, q.shape, q.dtype, q.device)
+        self._check_act(out, L, "out")
+        handle, guard = _on(self.device, stream)
+        with guard:
+            _check(lib().unstep_q8_window_attn(_dev_ptr(q, "q"), ctypes.byref(self.q8),
+                                               int(window), _dev_ptr(out, "out"), handle),
+                   "unstep_q8_window_attn")
+        return out
+
+    def read_frames(self, first_frame: int, frames: int, k_out: Optional[torch.Tensor] = None,
+                    v_out: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None
+                    ) -> Tuple[torch.Tensor, torch.Tensor]:
+        """K (rotated) and V of frames ``first_frame .. first_frame+frames-1`` in time order, as
+        bf16 ``[B][H][frames*Tf][D]``.  The ring must hold the frames."""
+        c = self.c
+        if frames < 1 or frames > c.cap_frames:
+            raise UnstepError(UNSTEP_ERR_WINDOW if frames > 0 else UNSTEP_ERR_ARG, "read_frames")
+        want = (c.B, c.H, frames * self.Tf, c.D)
+        outs = []
+        for t, n in ((k_out, "k_out"), (v_out, "v_out")):
+            if t is None:
+                t = _new_on(stream, want, torch.bfloat16, self.device)
+            elif t.dtype != torch.bfloat16 or tuple(t.shape) != want or t.device != self.device:
+                raise ValueError(f"{n} must be bfloat16 {want} on {self.device}")
+            outs.append(t)
+        handle, guard = _on(self.device, stream)
+        with guard:
+            _check(lib().unstep_q8_cache_read(ctypes.byref(self.q8), int(first_frame),
+                                              int(frames), _dev_ptr(outs[0], "k_out"),
+                                              _dev_ptr(outs[1], "v_out"), handle),
+                   "unstep_q8_cache_read")
+        return outs[0], outs[1]
+
+    def state_bytes(self) -> int:
+        return lib().unstep_q8_cache_state_bytes(ctypes.byref(self.q8))
+
+    def _save(self, ptr: int, n: int, handle: int) -> None:
+        _check(lib().unstep_q8_cache_save(ctypes.byref(self.q8), ptr, n, handle),
+               "unstep_q8_cache_save")
+
+    def _restore(self, ptr: int, n: int, handle: int) -> None:
+        _check(lib().unstep_q8_cache_restore(ctypes.byref(self.q8), ptr, n, handle),
+               "unstep_q8_cache_restore")
 
 
 class HostStepPipeline:
@@ -560,6 +744,166 @@ def renoise(x0: torch.Tensor, eps: torch.Tensor, sigma: float,
                                 x0.numel(), float(sigma), _stream_handle(stream)),
            "unstep_renoise")
     return out
+
+
+class Norm(NamedTuple):
+    """One norm over the last axis, in fp32: LayerNorm (``"layer"``) or RMS norm (``"rms"``), then
+    ``(n * weight + bias) * (1 + scale) + shift``; what is None is left out.
+
+    ``weight`` and ``bias`` are ``[C]``; ``scale`` and ``shift`` ``[G][C]`` (rows may be strided,
+    as columns of one conditioning table are): the tensor's rows are split evenly, in order, into
+    G groups (a chunk's frames) with a modulation each.  All bf16 or all fp32.
+    """
+    kind: str = "layer"
+    eps: float = 1e-6
+    weight: Optional[torch.Tensor] = None
+    bias: Optional[torch.Tensor] = None
+    scale: Optional[torch.Tensor] = None
+    shift: Optional[torch.Tensor] = None
+
+
+_NORM_KINDS = {"layer": UNSTEP_NORM_LAYER, "rms": UNSTEP_NORM_RMS}
+_TYPES = {torch.bfloat16: UNSTEP_BF16, torch.float32: UNSTEP_F32}
+
+
+def _rows_of(t: torch.Tensor, name: str) -> Tuple[int, int]:
+    """(rows, row stride) of a tensor whose last axis is contiguous and whose leading axes walk
+    its rows at one stride."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) < 2:
+        raise ValueError(f"{name} must have a row axis and a channel axis")
+    if shape[-1] > 1 and strides[-1] != 1:
+        raise ValueError(f"{name}'s channels must be contiguous")
+    if t.numel() == 0:
+        return 0, shape[-1]
+    rows, ld = 1, shape[-1]
+    for n, st in zip(reversed(shape[:-1]), reversed(strides[:-1])):
+        if n != 1:
+            if rows == 1:
+                ld = st
+            elif st != ld * rows:
+                raise ValueError(f"{name}'s rows must lie at one stride")
+        rows *= n
+    if ld < shape[-1]:
+        raise ValueError(f"{name}'s rows must not overlap")
+    return rows, ld
+
+
+def _vectors(t: Optional[torch.Tensor], C: int, groups: Optional[int], rows: int, name: str,
+             dev: torch.device) -> Tuple[Optional[int], int, Optional[int]]:
+    """(pointer, group stride, groups) of a [G][C] modulation tensor."""
+    if t is None:
+        return None, 0, groups
+    if t.dim() != 2 or t.shape[1] != C or t.stride(1) != 1 or t.device != dev or \
+            t.dtype not in _TYPES:
+        raise ValueError(f"{name} must be bf16 or fp32 [groups][{C}] on {dev}, channels contiguous")
+    G = t.shape[0]
+    if G < 1 or rows % G or (groups is not None and groups != G):
+        raise ValueError(f"{name} has {G} groups for {rows} rows"
+                         + ("" if groups is None else f", other modulations {groups}"))
+    return t.data_ptr(), (t.stride(0) if G > 1 else 0), G
+
+
+def _norm_struct(n: Norm, C: int, rows: int, groups: Optional[int], dev: torch.device):
+    """(unstep_norm_t, groups) of a Norm for `rows` rows of C channels."""
+    kind = _NORM_KINDS.get(n.kind)
+    if kind is None:
+        raise ValueError(f"norm kind {n.kind!r}: 'layer' or 'rms'")
+    types = {t.dtype for t in n[2:] if t is not None}
+    if len(types) > 1 or not types <= _TYPES.keys():
+        raise ValueError("a norm's weight, bias, scale and shift must be all bf16 or all fp32")
+    s = unstep_norm_t()
+    s.kind, s.eps = kind, n.eps
+    s.param_type = _TYPES[types.pop()] if types else UNSTEP_F32
+    for name in ("weight", "bias"):
+        t = getattr(n, name)
+        if t is not None:
+            if t.shape != (C,) or not t.is_contiguous() or t.device != dev:
+                raise ValueError(f"{name} must be contiguous [{C}] on {dev}")
+            setattr(s, name, t.data_ptr())
+    s.scale, ld, groups = _vectors(n.scale, C, groups, rows, "scale", dev)
+    s.shift, ld2, groups = _vectors(n.shift, C, groups, rows, "shift", dev)
+    if n.scale is not None and n.shift is not None and ld != ld2:
+        raise ValueError("scale and shift must have the same row stride")
+    s.mod_stride = ld or ld2
+    return s, groups
+
+
+def _norm_out(t: Optional[torch.Tensor], like: torch.Tensor, dtype: torch.dtype, name: str,
+              stream: Optional[torch.cuda.Stream]) -> Tuple[torch.Tensor, int]:
+    """(output, row stride): `t` checked against `like`, or a new contiguous tensor."""
+    if t is None:
+        t = _new_on(stream, like.shape, dtype, like.device)
+        return t, like.shape[-1]
+    if t.shape != like.shape or t.dtype != dtype or t.device != like.device:
+        raise ValueError(f"{name} must be {dtype} {tuple(like.shape)} on {like.device}")
+    return t, _rows_of(t, name)[1]
+
+
+def norm_modulate(x: torch.Tensor, norm: Norm, out: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """``norm`` of every row of x (bf16 or fp32 ``[..., C]``, rows at one stride) as bf16.
+
+    The norm and modulation before a DiT block, or with a weight alone the norm of projected
+    queries and keys.  ``out`` may be x itself when x is bf16.
+    """
+    if not x.is_cuda or x.dtype not in _TYPES:
+        raise ValueError("x must be a bf16 or fp32 CUDA tensor")
+    rows, ldx = _rows_of(x, "x")
+    C = x.shape[-1]
+    spec, groups = _norm_struct(norm, C, rows, None, x.device)
+    out, ldo = _norm_out(out, x, torch.bfloat16, "out", stream)
+    handle, guard = _on(x.device, stream)
+    with guard:
+        _check(lib().unstep_norm_modulate(x.data_ptr(), _TYPES[x.dtype], ldx, out.data_ptr(), ldo,
+                                          rows, C, max(1, rows // (groups or 1)),
+                                          ctypes.byref(spec), handle), "unstep_norm_modulate")
+    return out
+
+
+def gate_residual_norm(x: torch.Tensor, y: torch.Tensor, gate: Optional[torch.Tensor] = None,
+                       res_scale: float = 1.0, post: Optional[Norm] = None,
+                       next: Optional[Norm] = None, x_out: Optional[torch.Tensor] = None,
+                       out: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None
+                       ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """``x_out = x + res_scale * gate * post(y)`` and ``out = next(x_out)``: the end of a DiT block
+    and the norm before the next, in one pass.
+
+    x: the residual stream, bf16 or fp32 ``[..., C]``; y: the block's output, bf16 of x's shape;
+    gate: ``[G][C]`` as a Norm's scale, or None for 1.  ``x_out`` None updates x in place;
+    ``next`` None leaves the second output out (None).  ``next`` sees the fp32 sum, before it is
+    rounded to x's type.  Returns (x_out, out).
+    """
+    if not x.is_cuda or x.dtype not in _TYPES:
+        raise ValueError("x must be a bf16 or fp32 CUDA tensor")
+    if y.dtype != torch.bfloat16 or y.shape != x.shape or y.device != x.device:
+        raise ValueError(f"y must be bfloat16 {tuple(x.shape)} on {x.device}")
+    rows, ldx = _rows_of(x, "x")
+    ldy = _rows_of(y, "y")[1]
+    C, dev = x.shape[-1], x.device
+    gp, gs, groups = _vectors(gate, C, None, rows, "gate", dev)
+    post_s = next_s = None
+    if post is not None:
+        post_s, groups = _norm_struct(post, C, rows, groups, dev)
+    if next is not None:
+        next_s, groups = _norm_struct(next, C, rows, groups, dev)
+    elif out is not None:
+        raise ValueError("out without a next norm")
+    x_out, ldxo = (x, ldx) if x_out is None else _norm_out(x_out, x, x.dtype, "x_out", stream)
+    op, ldo = None, 0
+    if next is not None:
+        out, ldo = _norm_out(out, x, torch.bfloat16, "out", stream)
+        op = out.data_ptr()
+    handle, guard = _on(dev, stream)
+    with guard:
+        _check(lib().unstep_gate_residual_norm(
+            x.data_ptr(), _TYPES[x.dtype], ldx, y.data_ptr(), ldy, gp,
+            UNSTEP_F32 if gate is None else _TYPES[gate.dtype], gs, float(res_scale),
+            None if post_s is None else ctypes.byref(post_s),
+            None if next_s is None else ctypes.byref(next_s), x_out.data_ptr(), ldxo, op, ldo,
+            rows, C, max(1, rows // (groups or 1)), handle), "unstep_gate_residual_norm")
+    return x_out, out
 
 
 def selftest_wait_timeout(dev_error: torch.Tensor, limit_ns: int,

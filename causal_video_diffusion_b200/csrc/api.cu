@@ -16,13 +16,15 @@
 #include <cuda_runtime.h>
 
 #include "../../include/unstep.h"
+#include "block_norm.h"
 #include "conv3d.h"
 #include "gemm.h"
 #include "internal.h"
 
 namespace {
 
-constexpr int kInitMagic = 0x55535450;  // "USTP"
+constexpr int kInitMagic = 0x55535450;    // "USTP": an initialised bf16 cache
+constexpr int kInitMagicQ8 = 0x55535138;  // "USQ8": the base of an initialised 8-bit cache
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -60,6 +62,11 @@ size_t table_floats(const unstep_cache_t *c) {
   return 2ull * (static_cast<size_t>(c->max_pos_t) * (c->d_t / 2) +
                  static_cast<size_t>(c->Hg) * (c->d_h / 2) +
                  static_cast<size_t>(c->Wg) * (c->d_w / 2));
+}
+
+// Initialised as a bf16 cache or as the base of an 8-bit one (host-side plans take both).
+bool is_initialized(const unstep_cache_t *c) {
+  return c->initialized == kInitMagic || c->initialized == kInitMagicQ8;
 }
 
 int check_ready(const unstep_cache_t *c) {
@@ -131,7 +138,8 @@ size_t scratch_bytes_for(const unstep_cache_t *c, int sms) {
 }
 
 // ---- checkpoint buffer header (layout documented with unstep_cache_save) ----
-constexpr int kStateMagic = 0x43545355;  // "USTC"
+constexpr int kStateMagic = 0x43545355;    // "USTC"
+constexpr int kStateMagicQ8 = 0x51545355;  // "USTQ": an 8-bit cache
 constexpr int kStateVersion = 1;
 constexpr size_t kStateSlotOffset = 128;
 
@@ -146,10 +154,10 @@ int get_i32(const unsigned char *p, size_t off) {
   return v;
 }
 
-void write_state_header(const unstep_cache_t *c, unsigned char *p) {
+void write_state_header(const unstep_cache_t *c, int magic, unsigned char *p) {
   const int f[14] = {c->B,  c->H,          c->D,         c->Hg,  c->Wg,  c->d_t, c->d_h,
                      c->d_w, c->cap_frames, c->max_pos_t, act_B(c), act_H(c), c->b0, c->h0};
-  put_i32(p, 0, kStateMagic);
+  put_i32(p, 0, magic);
   put_i32(p, 4, kStateVersion);
   for (int i = 0; i < 14; ++i) put_i32(p, 8 + 4 * i, f[i]);
   std::memcpy(p + 64, &c->theta, sizeof(double));
@@ -159,8 +167,8 @@ void write_state_header(const unstep_cache_t *c, unsigned char *p) {
   put_i32(p, 84, c->last_chunk_frames);
 }
 
-int read_state_header(const unsigned char *p, unstep_cache_t *c) {
-  if (get_i32(p, 0) != kStateMagic || get_i32(p, 4) != kStateVersion) return UNSTEP_ERR_ARG;
+int read_state_header(const unsigned char *p, int magic, unstep_cache_t *c) {
+  if (get_i32(p, 0) != magic || get_i32(p, 4) != kStateVersion) return UNSTEP_ERR_ARG;
   int *f[14] = {&c->B,  &c->H,          &c->D,         &c->Hg,    &c->Wg,    &c->d_t, &c->d_h,
                 &c->d_w, &c->cap_frames, &c->max_pos_t, &c->act_B, &c->act_H, &c->b0,  &c->h0};
   for (int i = 0; i < 14; ++i) *f[i] = get_i32(p, 8 + 4 * i);
@@ -179,6 +187,106 @@ bool same_state_shape(const unstep_cache_t *a, const unstep_cache_t *b) {
          a->cap_frames == b->cap_frames && a->max_pos_t == b->max_pos_t &&
          act_B(a) == act_B(b) && act_H(a) == act_H(b) && a->b0 == b->b0 && a->h0 == b->h0 &&
          std::memcmp(&a->theta, &b->theta, sizeof(double)) == 0;
+}
+
+// What unstep_cache_init and unstep_q8_cache_init share: checks, coefficient tables, `kvb` zeroed
+// bytes of each of K and V, slots, counters and metadata.
+int init_cache(unstep_cache_t *cache, size_t kvb, int magic, cudaStream_t s) {
+  int rc = check_shape(cache);
+  if (rc) return rc;
+  if (!cache->k_cache || !cache->v_cache || !cache->slot_frame || !cache->cos_sin ||
+      !cache->dev_error)
+    return UNSTEP_ERR_ARG;
+  if (!aligned16(cache->k_cache) || !aligned16(cache->v_cache) || !aligned16(cache->cos_sin) ||
+      !aligned16(cache->attn_scratch))
+    return UNSTEP_ERR_ALIGN;
+  if (cache->attn_scratch) {
+    const int sms = device_sms();
+    if (sms <= 0) return UNSTEP_ERR_CUDA;
+    if (cache->attn_scratch_bytes < scratch_bytes_for(cache, sms)) return UNSTEP_ERR_ARG;
+  }
+  // cached coefficients: cos/sin of pos * theta^(-2j/d_a), computed in fp64, stored fp32
+  std::vector<float> tab(table_floats(cache));
+  size_t o = 0;
+  const int dims[3] = {cache->d_t, cache->d_h, cache->d_w};
+  const int npos[3] = {cache->max_pos_t, cache->Hg, cache->Wg};
+  for (int a = 0; a < 3; ++a) {
+    const int half = dims[a] / 2;
+    for (int pos = 0; pos < npos[a]; ++pos) {
+      for (int j = 0; j < half; ++j) {
+        const double inv = std::pow(cache->theta, -2.0 * j / static_cast<double>(dims[a]));
+        const double ang = static_cast<double>(pos) * inv;
+        tab[o++] = static_cast<float>(std::cos(ang));
+        tab[o++] = static_cast<float>(std::sin(ang));
+      }
+    }
+  }
+  if (cudaMemcpyAsync(cache->cos_sin, tab.data(), tab.size() * sizeof(float),
+                      cudaMemcpyHostToDevice, s) != cudaSuccess ||
+      cudaMemsetAsync(cache->k_cache, 0, kvb, s) != cudaSuccess ||
+      cudaMemsetAsync(cache->v_cache, 0, kvb, s) != cudaSuccess ||
+      cudaMemsetAsync(cache->slot_frame, 0xFF, sizeof(int) * cache->cap_frames, s) !=
+          cudaSuccess ||
+      cudaMemsetAsync(cache->dev_error, 0, sizeof(int), s) != cudaSuccess ||
+      (cache->attn_scratch &&
+       cudaMemsetAsync(cache->attn_scratch, 0, unstep::attn_counter_bytes(max_units(cache)), s) !=
+           cudaSuccess)) {
+    cudaGetLastError();
+    return UNSTEP_ERR_CUDA;
+  }
+  cache->frames_written = 0;
+  cache->first_frame = 0;
+  cache->last_chunk_start = -1;
+  cache->last_chunk_frames = 0;
+  cache->initialized = magic;
+  return UNSTEP_OK;
+}
+
+// Launch parameters of an append, all but the queries.
+unstep::RopeAppendParams append_params(const unstep_cache_t *cache, const void *k, const void *v,
+                                       int frame_idx, unstep_grid_t grid) {
+  unstep::RopeAppendParams p{};
+  p.k = k;
+  p.v = v;
+  p.k_cache = cache->k_cache;
+  p.v_cache = cache->v_cache;
+  p.slot_frame = cache->slot_frame;
+  const float2 *tab = reinterpret_cast<const float2 *>(cache->cos_sin);
+  p.tab_t = tab;
+  p.tab_h = p.tab_t + static_cast<size_t>(cache->max_pos_t) * (cache->d_t / 2);
+  p.tab_w = p.tab_h + static_cast<size_t>(cache->Hg) * (cache->d_h / 2);
+  p.B = cache->B;
+  p.H = cache->H;
+  p.act_H = act_H(cache);
+  p.b0 = cache->b0;
+  p.h0 = cache->h0;
+  p.sharded = (p.act_H != p.H || p.b0 != 0 || p.h0 != 0) ? 1 : 0;
+  p.D = cache->D;
+  p.Hg = cache->Hg;
+  p.Wg = cache->Wg;
+  p.Tf = cache->Hg * cache->Wg;
+  p.L = grid.frames * p.Tf;
+  p.half_t = cache->d_t / 2;
+  p.half_h = cache->d_h / 2;
+  p.half_w = cache->d_w / 2;
+  p.frame_idx = frame_idx;
+  p.frames = grid.frames;
+  p.cap = cache->cap_frames;
+  p.rows = cache->cap_frames * p.Tf;
+  p.act_B = act_B(cache);
+  p.max_pos_t = cache->max_pos_t;
+  p.dev_error = cache->dev_error;
+  return p;
+}
+
+// Metadata after an append was launched.
+void note_append(unstep_cache_t *cache, int frame_idx, int frames, bool is_new) {
+  if (is_new) {
+    if (cache->last_chunk_frames == 0) cache->first_frame = frame_idx;
+    cache->frames_written = frame_idx + frames;
+  }
+  cache->last_chunk_start = frame_idx;
+  cache->last_chunk_frames = frames;
 }
 
 unsigned next_epoch() {
@@ -230,63 +338,17 @@ size_t unstep_attn_scratch_bytes(const unstep_cache_t *cache) {
 }
 
 int unstep_cache_init(unstep_cache_t *cache, unstep_stream_t stream) {
-  int rc = check_shape(cache);
-  if (rc) return rc;
-  if (!cache->k_cache || !cache->v_cache || !cache->slot_frame || !cache->cos_sin ||
-      !cache->dev_error)
-    return UNSTEP_ERR_ARG;
-  if (!aligned16(cache->k_cache) || !aligned16(cache->v_cache) || !aligned16(cache->cos_sin) ||
-      !aligned16(cache->attn_scratch))
-    return UNSTEP_ERR_ALIGN;
-  if (cache->attn_scratch) {
-    const int sms = device_sms();
-    if (sms <= 0) return UNSTEP_ERR_CUDA;
-    if (cache->attn_scratch_bytes < scratch_bytes_for(cache, sms)) return UNSTEP_ERR_ARG;
-  }
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  // cached coefficients: cos/sin of pos * theta^(-2j/d_a), computed in fp64, stored fp32
-  std::vector<float> tab(table_floats(cache));
-  size_t o = 0;
-  const int dims[3] = {cache->d_t, cache->d_h, cache->d_w};
-  const int npos[3] = {cache->max_pos_t, cache->Hg, cache->Wg};
-  for (int a = 0; a < 3; ++a) {
-    const int half = dims[a] / 2;
-    for (int pos = 0; pos < npos[a]; ++pos) {
-      for (int j = 0; j < half; ++j) {
-        const double inv = std::pow(cache->theta, -2.0 * j / static_cast<double>(dims[a]));
-        const double ang = static_cast<double>(pos) * inv;
-        tab[o++] = static_cast<float>(std::cos(ang));
-        tab[o++] = static_cast<float>(std::sin(ang));
-      }
-    }
-  }
-  const size_t kvb = unstep_cache_kv_bytes(cache);
-  if (cudaMemcpyAsync(cache->cos_sin, tab.data(), tab.size() * sizeof(float),
-                      cudaMemcpyHostToDevice, s) != cudaSuccess ||
-      cudaMemsetAsync(cache->k_cache, 0, kvb, s) != cudaSuccess ||
-      cudaMemsetAsync(cache->v_cache, 0, kvb, s) != cudaSuccess ||
-      cudaMemsetAsync(cache->slot_frame, 0xFF, sizeof(int) * cache->cap_frames, s) !=
-          cudaSuccess ||
-      cudaMemsetAsync(cache->dev_error, 0, sizeof(int), s) != cudaSuccess ||
-      (cache->attn_scratch &&
-       cudaMemsetAsync(cache->attn_scratch, 0, unstep::attn_counter_bytes(max_units(cache)), s) !=
-           cudaSuccess)) {
-    cudaGetLastError();
-    return UNSTEP_ERR_CUDA;
-  }
-  cache->frames_written = 0;
-  cache->first_frame = 0;
-  cache->last_chunk_start = -1;
-  cache->last_chunk_frames = 0;
-  cache->initialized = kInitMagic;
-  return UNSTEP_OK;
+  // the base of an 8-bit cache has buffers of another size: unstep_q8_cache_init resets it
+  if (cache && cache->initialized == kInitMagicQ8) return UNSTEP_ERR_ARG;
+  return init_cache(cache, unstep_cache_kv_bytes(cache), kInitMagic,
+                    reinterpret_cast<cudaStream_t>(stream));
 }
 
 int unstep_append_plan(const unstep_cache_t *cache, int frame_idx, unstep_grid_t grid,
                        int *slots_out) {
   int rc = check_shape(cache);
   if (rc) return rc;
-  if (cache->initialized != kInitMagic) return UNSTEP_ERR_ARG;
+  if (!is_initialized(cache)) return UNSTEP_ERR_ARG;
   if (grid.Hg != cache->Hg || grid.Wg != cache->Wg || grid.frames < 1) return UNSTEP_ERR_SHAPE;
   if (grid.frames > cache->cap_frames) return UNSTEP_ERR_WINDOW;
   if (frame_idx < 0 || static_cast<long long>(frame_idx) + grid.frames > cache->max_pos_t)
@@ -317,49 +379,14 @@ int unstep_rope_kv_append_ex(void *q, const void *k, const void *v, unstep_cache
   if ((rotate_q && !aligned16(q)) || !aligned16(k) || !aligned16(v)) return UNSTEP_ERR_ALIGN;
   const int is_new = unstep_append_plan(cache, frame_idx, grid, nullptr);
   if (is_new < 0) return is_new;
-  unstep::RopeAppendParams p{};
+  unstep::RopeAppendParams p = append_params(cache, k, v, frame_idx, grid);
   p.q = rotate_q ? q : nullptr;
   p.rotate_q = rotate_q ? 1 : 0;
-  p.k = k;
-  p.v = v;
-  p.k_cache = cache->k_cache;
-  p.v_cache = cache->v_cache;
-  p.slot_frame = cache->slot_frame;
-  const float2 *tab = reinterpret_cast<const float2 *>(cache->cos_sin);
-  p.tab_t = tab;
-  p.tab_h = p.tab_t + static_cast<size_t>(cache->max_pos_t) * (cache->d_t / 2);
-  p.tab_w = p.tab_h + static_cast<size_t>(cache->Hg) * (cache->d_h / 2);
-  p.B = cache->B;
-  p.H = cache->H;
-  p.act_H = act_H(cache);
-  p.b0 = cache->b0;
-  p.h0 = cache->h0;
-  p.sharded = (p.act_H != p.H || p.b0 != 0 || p.h0 != 0) ? 1 : 0;
-  p.D = cache->D;
-  p.Hg = cache->Hg;
-  p.Wg = cache->Wg;
-  p.Tf = cache->Hg * cache->Wg;
-  p.L = grid.frames * p.Tf;
-  p.half_t = cache->d_t / 2;
-  p.half_h = cache->d_h / 2;
-  p.half_w = cache->d_w / 2;
-  p.frame_idx = frame_idx;
-  p.frames = grid.frames;
-  p.cap = cache->cap_frames;
-  p.rows = cache->cap_frames * p.Tf;
-  p.act_B = act_B(cache);
-  p.max_pos_t = cache->max_pos_t;
-  p.dev_error = cache->dev_error;
   if (unstep::launch_rope_kv_append(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) {
     cudaGetLastError();
     return UNSTEP_ERR_CUDA;
   }
-  if (is_new) {
-    if (cache->last_chunk_frames == 0) cache->first_frame = frame_idx;
-    cache->frames_written = frame_idx + grid.frames;
-  }
-  cache->last_chunk_start = frame_idx;
-  cache->last_chunk_frames = grid.frames;
+  note_append(cache, frame_idx, grid.frames, is_new == 1);
   return UNSTEP_OK;
 }
 
@@ -371,7 +398,7 @@ int unstep_rope_kv_append(void *q, const void *k, const void *v, unstep_cache_t 
 int unstep_window_plan(const unstep_cache_t *cache, int window, unstep_window_plan_t *plan) {
   int rc = check_shape(cache);
   if (rc) return rc;
-  if (!plan || cache->initialized != kInitMagic) return UNSTEP_ERR_ARG;
+  if (!plan || !is_initialized(cache)) return UNSTEP_ERR_ARG;
   if (cache->last_chunk_frames < 1) return UNSTEP_ERR_WINDOW;
   if (window < cache->last_chunk_frames || window > cache->cap_frames) return UNSTEP_ERR_WINDOW;
   const int tf = cache->Hg * cache->Wg;
@@ -723,7 +750,7 @@ int unstep_cache_save(const unstep_cache_t *cache, void *host_dst, size_t bytes,
   unsigned char *dst = static_cast<unsigned char *>(host_dst);
   const size_t hb = state_header_bytes(cache), kvb = unstep_cache_kv_bytes(cache);
   std::memset(dst, 0, hb);
-  write_state_header(cache, dst);
+  write_state_header(cache, kStateMagic, dst);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (cudaMemcpyAsync(dst + kStateSlotOffset, cache->slot_frame,
                       sizeof(int) * cache->cap_frames, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
@@ -743,7 +770,7 @@ int unstep_cache_restore(unstep_cache_t *cache, const void *host_src, size_t byt
   if (!host_src || bytes < kStateSlotOffset) return UNSTEP_ERR_ARG;
   const unsigned char *src = static_cast<const unsigned char *>(host_src);
   unstep_cache_t saved{};
-  rc = read_state_header(src, &saved);
+  rc = read_state_header(src, kStateMagic, &saved);
   if (rc) return rc;
   if (!same_state_shape(cache, &saved)) return UNSTEP_ERR_SHAPE;
   if (bytes < unstep_cache_state_bytes(cache)) return UNSTEP_ERR_ARG;
@@ -765,6 +792,349 @@ int unstep_cache_restore(unstep_cache_t *cache, const void *host_src, size_t byt
   cache->first_frame = saved.first_frame;
   cache->last_chunk_start = saved.last_chunk_start;
   cache->last_chunk_frames = saved.last_chunk_frames;
+  return UNSTEP_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// An initialised 8-bit cache: its base's checks under its own magic, and the scale pointers.
+int check_ready_q8(const unstep_q8_cache_t *c) {
+  if (!c) return UNSTEP_ERR_ARG;
+  int rc = check_shape(&c->base);
+  if (rc) return rc;
+  if (c->base.initialized != kInitMagicQ8) return UNSTEP_ERR_ARG;
+  if (!c->base.k_cache || !c->base.v_cache || !c->base.slot_frame || !c->base.cos_sin ||
+      !c->base.dev_error || !c->k_scale || !c->v_scale)
+    return UNSTEP_ERR_ARG;
+  return UNSTEP_OK;
+}
+
+// Ring rows of `count` frames from frame f0 on: at most two ranges.
+void ring_rows(const unstep_cache_t *c, int f0, int count, int (&row)[2], int (&len)[2]) {
+  const int tf = c->Hg * c->Wg, s0 = f0 % c->cap_frames;
+  const int n0 = count < c->cap_frames - s0 ? count : c->cap_frames - s0;
+  row[0] = s0 * tf;
+  len[0] = n0 * tf;
+  row[1] = 0;
+  len[1] = (count - n0) * tf;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t unstep_q8_cache_kv_bytes(const unstep_q8_cache_t *cache) {
+  return cache ? unstep_cache_kv_bytes(&cache->base) / 2 : 0;
+}
+
+size_t unstep_q8_cache_scale_bytes(const unstep_q8_cache_t *cache) {
+  return unstep_q8_cache_kv_bytes(cache) / 32;
+}
+
+int unstep_q8_cache_init(unstep_q8_cache_t *cache, unstep_stream_t stream) {
+  if (!cache) return UNSTEP_ERR_ARG;
+  int rc = check_shape(&cache->base);
+  if (rc) return rc;
+  if (!cache->k_scale || !cache->v_scale) return UNSTEP_ERR_ARG;
+  if (!aligned16(cache->k_scale) || !aligned16(cache->v_scale)) return UNSTEP_ERR_ALIGN;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  rc = init_cache(&cache->base, unstep_q8_cache_kv_bytes(cache), kInitMagicQ8, s);
+  if (rc) return rc;
+  const size_t sb = unstep_q8_cache_scale_bytes(cache);
+  if (cudaMemsetAsync(cache->k_scale, 0, sb, s) != cudaSuccess ||
+      cudaMemsetAsync(cache->v_scale, 0, sb, s) != cudaSuccess) {
+    cudaGetLastError();
+    cache->base.initialized = 0;
+    return UNSTEP_ERR_CUDA;
+  }
+  return UNSTEP_OK;
+}
+
+int unstep_q8_rope_kv_append(const void *q, void *q_out, const void *k, const void *v,
+                             unstep_q8_cache_t *cache, int frame_idx, unstep_grid_t grid,
+                             unstep_stream_t stream) {
+  int rc = check_ready_q8(cache);
+  if (rc) return rc;
+  if (!q || !q_out || !k || !v) return UNSTEP_ERR_ARG;
+  if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(v))
+    return UNSTEP_ERR_ALIGN;
+  unstep_cache_t *c = &cache->base;
+  const int is_new = unstep_append_plan(c, frame_idx, grid, nullptr);
+  if (is_new < 0) return is_new;
+  const long long rows = static_cast<long long>(grid.frames) * c->Hg * c->Wg;
+  if (rows > INT_MAX || static_cast<long long>(c->B) * c->H > (1ll << 31) / (c->D / 8) / rows - 1)
+    return UNSTEP_ERR_UNSUPPORTED;
+  unstep::Q8AppendParams p{};
+  p.rope = append_params(c, k, v, frame_idx, grid);
+  p.rope.q = const_cast<void *>(q);  // read only
+  p.rope.rotate_q = 1;
+  p.q_out = q_out;
+  p.k_scale = static_cast<unsigned char *>(cache->k_scale);
+  p.v_scale = static_cast<unsigned char *>(cache->v_scale);
+  if (unstep::launch_q8_rope_kv_append(p, reinterpret_cast<cudaStream_t>(stream)) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return UNSTEP_ERR_CUDA;
+  }
+  note_append(c, frame_idx, grid.frames, is_new == 1);
+  return UNSTEP_OK;
+}
+
+int unstep_q8_window_attn(const void *q, const unstep_q8_cache_t *cache, int window, void *out,
+                          unstep_stream_t stream) {
+  int rc = check_ready_q8(cache);
+  if (rc) return rc;
+  if (!q || !out) return UNSTEP_ERR_ARG;
+  if (!aligned16(q) || !aligned16(out)) return UNSTEP_ERR_ALIGN;
+  const unstep_cache_t *c = &cache->base;
+  unstep_window_plan_t plan;
+  rc = unstep_window_plan(c, window, &plan);
+  if (rc) return rc;
+  unstep::Q8AttnParams p{};
+  unstep::AttnParams &a = p.attn;
+  a.out = out;
+  a.dev_error = c->dev_error;
+  a.B = c->B;
+  a.H = c->H;
+  a.act_H = act_H(c);
+  a.act_B = act_B(c);
+  a.b0 = c->b0;
+  a.h0 = c->h0;
+  a.L = c->last_chunk_frames * c->Hg * c->Wg;
+  a.rows = c->cap_frames * c->Hg * c->Wg;
+  for (int s = 0; s < 2; ++s) {
+    a.seg_row[s] = plan.seg_row[s];
+    a.seg_len[s] = plan.seg_len[s];
+  }
+  a.scale_log2 =
+      static_cast<float>(1.4426950408889634073599 / std::sqrt(static_cast<double>(c->D)));
+  p.q = q;
+  p.k_cache = static_cast<const unsigned char *>(c->k_cache);
+  p.v_cache = static_cast<const unsigned char *>(c->v_cache);
+  p.k_scale = static_cast<const unsigned char *>(cache->k_scale);
+  p.v_scale = static_cast<const unsigned char *>(cache->v_scale);
+  if (unstep::launch_q8_window_attn(c->D, p, reinterpret_cast<cudaStream_t>(stream)) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return UNSTEP_ERR_CUDA;
+  }
+  return UNSTEP_OK;
+}
+
+int unstep_q8_cache_read(const unstep_q8_cache_t *cache, int first_frame, int frames, void *k_out,
+                         void *v_out, unstep_stream_t stream) {
+  int rc = check_ready_q8(cache);
+  if (rc) return rc;
+  if ((!k_out && !v_out) || frames < 1) return UNSTEP_ERR_ARG;
+  if (!aligned16(k_out) || !aligned16(v_out)) return UNSTEP_ERR_ALIGN;
+  const unstep_cache_t *c = &cache->base;
+  const long long end = static_cast<long long>(first_frame) + frames;
+  if (c->last_chunk_frames < 1 || first_frame < c->first_frame || end > c->frames_written ||
+      first_frame < c->frames_written - c->cap_frames)
+    return UNSTEP_ERR_WINDOW;
+  unstep::Q8ReadParams p{};
+  p.k_cache = static_cast<const unsigned char *>(c->k_cache);
+  p.v_cache = static_cast<const unsigned char *>(c->v_cache);
+  p.k_scale = static_cast<const unsigned char *>(cache->k_scale);
+  p.v_scale = static_cast<const unsigned char *>(cache->v_scale);
+  p.k_out = k_out;
+  p.v_out = v_out;
+  p.heads = c->B * c->H;
+  p.D = c->D;
+  p.rows = static_cast<long long>(c->cap_frames) * c->Hg * c->Wg;
+  p.n_rows = frames * c->Hg * c->Wg;
+  ring_rows(c, first_frame, frames, p.seg_row, p.seg_len);
+  if (unstep::launch_q8_cache_read(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return UNSTEP_ERR_CUDA;
+  }
+  return UNSTEP_OK;
+}
+
+size_t unstep_q8_cache_state_bytes(const unstep_q8_cache_t *cache) {
+  if (!cache || check_shape(&cache->base)) return 0;
+  return state_header_bytes(&cache->base) + 2 * unstep_q8_cache_kv_bytes(cache) +
+         2 * unstep_q8_cache_scale_bytes(cache);
+}
+
+int unstep_q8_cache_save(const unstep_q8_cache_t *cache, void *host_dst, size_t bytes,
+                         unstep_stream_t stream) {
+  int rc = check_ready_q8(cache);
+  if (rc) return rc;
+  if (!host_dst || bytes < unstep_q8_cache_state_bytes(cache)) return UNSTEP_ERR_ARG;
+  const unstep_cache_t *c = &cache->base;
+  unsigned char *dst = static_cast<unsigned char *>(host_dst);
+  const size_t hb = state_header_bytes(c), kvb = unstep_q8_cache_kv_bytes(cache),
+               sb = unstep_q8_cache_scale_bytes(cache);
+  std::memset(dst, 0, hb);
+  write_state_header(c, kStateMagicQ8, dst);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaMemcpyKind down = cudaMemcpyDeviceToHost;
+  if (cudaMemcpyAsync(dst + kStateSlotOffset, c->slot_frame, sizeof(int) * c->cap_frames, down,
+                      s) != cudaSuccess ||
+      cudaMemcpyAsync(dst + hb, c->k_cache, kvb, down, s) != cudaSuccess ||
+      cudaMemcpyAsync(dst + hb + kvb, c->v_cache, kvb, down, s) != cudaSuccess ||
+      cudaMemcpyAsync(dst + hb + 2 * kvb, cache->k_scale, sb, down, s) != cudaSuccess ||
+      cudaMemcpyAsync(dst + hb + 2 * kvb + sb, cache->v_scale, sb, down, s) != cudaSuccess) {
+    cudaGetLastError();
+    return UNSTEP_ERR_CUDA;
+  }
+  return UNSTEP_OK;
+}
+
+int unstep_q8_cache_restore(unstep_q8_cache_t *cache, const void *host_src, size_t bytes,
+                            unstep_stream_t stream) {
+  int rc = check_ready_q8(cache);
+  if (rc) return rc;
+  if (!host_src || bytes < kStateSlotOffset) return UNSTEP_ERR_ARG;
+  unstep_cache_t *c = &cache->base;
+  const unsigned char *src = static_cast<const unsigned char *>(host_src);
+  unstep_cache_t saved{};
+  rc = read_state_header(src, kStateMagicQ8, &saved);
+  if (rc) return rc;
+  if (!same_state_shape(c, &saved)) return UNSTEP_ERR_SHAPE;
+  if (bytes < unstep_q8_cache_state_bytes(cache)) return UNSTEP_ERR_ARG;
+  // the saved metadata must describe a ring this cache can hold: empty, or a latest chunk that
+  // ends at the newest frame and does not start before the stream
+  const long long chunk_end =
+      static_cast<long long>(saved.last_chunk_start) + saved.last_chunk_frames;
+  const bool empty = saved.last_chunk_frames == 0 && saved.last_chunk_start == -1 &&
+                     saved.frames_written == 0 && saved.first_frame == 0;
+  if (!empty && (saved.last_chunk_frames < 1 || saved.last_chunk_frames > c->cap_frames ||
+                 saved.first_frame < 0 || saved.last_chunk_start < saved.first_frame ||
+                 chunk_end != saved.frames_written || saved.frames_written > c->max_pos_t))
+    return UNSTEP_ERR_ARG;
+  const size_t hb = state_header_bytes(c), kvb = unstep_q8_cache_kv_bytes(cache),
+               sb = unstep_q8_cache_scale_bytes(cache);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaMemcpyKind up = cudaMemcpyHostToDevice;
+  if (cudaMemcpyAsync(c->slot_frame, src + kStateSlotOffset, sizeof(int) * c->cap_frames, up,
+                      s) != cudaSuccess ||
+      cudaMemcpyAsync(c->k_cache, src + hb, kvb, up, s) != cudaSuccess ||
+      cudaMemcpyAsync(c->v_cache, src + hb + kvb, kvb, up, s) != cudaSuccess ||
+      cudaMemcpyAsync(cache->k_scale, src + hb + 2 * kvb, sb, up, s) != cudaSuccess ||
+      cudaMemcpyAsync(cache->v_scale, src + hb + 2 * kvb + sb, sb, up, s) != cudaSuccess) {
+    cudaGetLastError();
+    return UNSTEP_ERR_CUDA;
+  }
+  c->frames_written = saved.frames_written;
+  c->first_frame = saved.first_frame;
+  c->last_chunk_start = saved.last_chunk_start;
+  c->last_chunk_frames = saved.last_chunk_frames;
+  return UNSTEP_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+bool known_type(int t) { return t == UNSTEP_BF16 || t == UNSTEP_F32; }
+
+// A norm's own fields: 0 or an error.
+int check_norm(const unstep_norm_t *n, int C) {
+  if (n->kind != UNSTEP_NORM_LAYER && n->kind != UNSTEP_NORM_RMS) return UNSTEP_ERR_ARG;
+  if (!(n->eps >= 0.f) || !std::isfinite(n->eps) || !known_type(n->param_type))
+    return UNSTEP_ERR_ARG;
+  if ((n->scale || n->shift) && (n->mod_stride < 0 || (n->mod_stride & 7))) return UNSTEP_ERR_SHAPE;
+  if (!aligned16(n->weight) || !aligned16(n->bias) || !aligned16(n->scale) || !aligned16(n->shift))
+    return UNSTEP_ERR_ALIGN;
+  return C > 0 ? UNSTEP_OK : UNSTEP_ERR_SHAPE;
+}
+
+// Sizes that both norm calls share.
+int check_rows(long long rows, int C, long long rows_per_group) {
+  if (rows < 0 || C < 8 || (C & 7) || rows_per_group < 1) return UNSTEP_ERR_SHAPE;
+  if (C > 16384) return UNSTEP_ERR_UNSUPPORTED;
+  return UNSTEP_OK;
+}
+
+bool bad_stride(long long ld, long long rows, int C) {
+  return (ld & 7) || ld < 0 || (rows > 1 && ld < C);
+}
+
+}  // namespace
+
+extern "C" {
+
+int unstep_norm_modulate(const void *x, int x_type, long long ldx, void *y, long long ldy,
+                         long long rows, int C, long long rows_per_group,
+                         const unstep_norm_t *norm, unstep_stream_t stream) {
+  if (!norm || !known_type(x_type)) return UNSTEP_ERR_ARG;
+  int rc = check_rows(rows, C, rows_per_group);
+  if (rc) return rc;
+  rc = check_norm(norm, C);
+  if (rc) return rc;
+  if (rows == 0) return UNSTEP_OK;
+  if (!x || !y) return UNSTEP_ERR_ARG;
+  if (bad_stride(ldx, rows, C) || bad_stride(ldy, rows, C)) return UNSTEP_ERR_SHAPE;
+  if (!aligned16(x) || !aligned16(y)) return UNSTEP_ERR_ALIGN;
+  if (y == x && (x_type != UNSTEP_BF16 || ldy != ldx)) return UNSTEP_ERR_ARG;
+  unstep::NormParams p{};
+  p.x = x;
+  p.x_type = x_type;
+  p.ldx = ldx;
+  p.h = y;
+  p.ldh = ldy;
+  p.rows = rows;
+  p.C = C;
+  p.rows_per_group = rows_per_group;
+  p.next = *norm;
+  if (unstep::launch_block_norm(p, false, reinterpret_cast<cudaStream_t>(stream)) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return UNSTEP_ERR_CUDA;
+  }
+  return UNSTEP_OK;
+}
+
+int unstep_gate_residual_norm(const void *x, int x_type, long long ldx, const void *y,
+                              long long ldy, const void *gate, int gate_type,
+                              long long gate_stride, float res_scale, const unstep_norm_t *post,
+                              const unstep_norm_t *next, void *x_out, long long ldxo, void *h,
+                              long long ldh, long long rows, int C, long long rows_per_group,
+                              unstep_stream_t stream) {
+  if (!known_type(x_type) || !known_type(gate_type) || !std::isfinite(res_scale))
+    return UNSTEP_ERR_ARG;
+  if ((next == nullptr) != (h == nullptr) && rows > 0) return UNSTEP_ERR_ARG;
+  int rc = check_rows(rows, C, rows_per_group);
+  if (rc) return rc;
+  if (post && (rc = check_norm(post, C))) return rc;
+  if (next && (rc = check_norm(next, C))) return rc;
+  if (rows == 0) return UNSTEP_OK;
+  if (!x || !y || !x_out) return UNSTEP_ERR_ARG;
+  if (bad_stride(ldx, rows, C) || bad_stride(ldy, rows, C) || bad_stride(ldxo, rows, C) ||
+      (h && bad_stride(ldh, rows, C)) || (gate && (gate_stride < 0 || (gate_stride & 7))))
+    return UNSTEP_ERR_SHAPE;
+  if (!aligned16(x) || !aligned16(y) || !aligned16(gate) || !aligned16(x_out) || !aligned16(h))
+    return UNSTEP_ERR_ALIGN;
+  if ((x_out == x && ldxo != ldx) || h == x || h == y || h == x_out || x_out == y)
+    return UNSTEP_ERR_ARG;
+  unstep::NormParams p{};
+  p.x = x;
+  p.x_type = x_type;
+  p.ldx = ldx;
+  p.y = y;
+  p.ldy = ldy;
+  p.gate = gate;
+  p.gate_type = gate_type;
+  p.gate_stride = gate_stride;
+  p.res_scale = res_scale;
+  p.x_out = x_out;
+  p.ldxo = ldxo;
+  p.h = h;
+  p.ldh = ldh;
+  p.rows = rows;
+  p.C = C;
+  p.rows_per_group = rows_per_group;
+  p.has_post = post ? 1 : 0;
+  if (post) p.post = *post;
+  if (next) p.next = *next;
+  if (unstep::launch_block_norm(p, true, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return UNSTEP_ERR_CUDA;
+  }
   return UNSTEP_OK;
 }
 

@@ -1,0 +1,169 @@
+// cache_q8.cu -- the 8-bit KV cache: fused 3D RoPE, quantisation and ring-buffer append, and the
+// rows read back as bf16.
+//
+// Append: the same streaming pass as the bf16 append (q, k, v read once), with the rotated k and
+// the v quantised in registers: the four lanes that hold a 32-channel block share its maximum by
+// two shuffles, then every lane writes the eight codes of its vector.  It moves 10 + 1/16 bytes
+// for every element of the chunk (q read and written, k and v read in bf16, two codes and their
+// share of two scale bytes) where the bf16 append moves 12.
+#include <cuda_bf16.h>
+
+#include "internal.h"
+#include "q8.cuh"
+#include "rope_append.cuh"
+
+namespace unstep {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr uint32_t kFullMask = 0xFFFFFFFFu;
+
+__device__ __forceinline__ void unpack8(const uint4 &w, float (&x)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(u[i] << 16);
+    x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+}
+
+// Rotates eight channels in fp32, unrounded (the codes are the only rounding of k).
+__device__ __forceinline__ void rotate8(float (&x)[8], const float2 (&cs)[4]) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const float a = x[2 * u], b = x[2 * u + 1];
+    x[2 * u] = __fmaf_rn(a, cs[u].x, -__fmul_rn(b, cs[u].y));
+    x[2 * u + 1] = __fmaf_rn(a, cs[u].y, __fmul_rn(b, cs[u].x));
+  }
+}
+
+// Codes of this lane's eight channels and the scale byte of its block (four lanes).
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], uint32_t &byte) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  m = max(m, __shfl_xor_sync(kFullMask, m, 1));
+  m = max(m, __shfl_xor_sync(kFullMask, m, 2));
+  byte = q8_scale_byte(m);
+  if (byte == kQ8NanByte) return make_uint2(0u, 0u);
+  const float inv = q8_inv_scale(byte), lim = byte == kQ8TopByte ? 240.f : 448.f;
+  return make_uint2(q8_encode2(x[0], x[1], inv, lim) | (q8_encode2(x[2], x[3], inv, lim) << 16),
+                    q8_encode2(x[4], x[5], inv, lim) | (q8_encode2(x[6], x[7], inv, lim) << 16));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) q8_rope_kv_append_kernel(const Q8AppendParams q,
+                                                                      uint32_t n_items) {
+  const RopeAppendParams &p = q.rope;
+  const uint32_t it = blockIdx.x * kThreads + threadIdx.x;
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < p.frames; i += kThreads) {
+      const int f = p.frame_idx + i;
+      if (debug_check(f >= 0 && p.cap > 0, p.dev_error)) p.slot_frame[f % p.cap] = f;
+    }
+  Item m;
+  // n_items is a multiple of a block's four lanes, so a block's lanes are live together
+  const bool live = it < n_items && locate<D>(p, it, m);
+  uint4 qv = make_uint4(0, 0, 0, 0), kv = qv, vv = qv;
+  if (live) {
+    qv = ld_plain(static_cast<const __nv_bfloat16 *>(p.q) + m.e);
+    kv = ld_stream(static_cast<const __nv_bfloat16 *>(p.k) + m.e);
+    vv = ld_stream(static_cast<const __nv_bfloat16 *>(p.v) + m.e);
+  } else {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) m.cs[u] = make_float2(0.f, 0.f);
+  }
+  float kx[8], vx[8];
+  unpack8(kv, kx);
+  unpack8(vv, vx);
+  rotate8(kx, m.cs);
+  uint32_t kb, vb;
+  const uint2 kc = quantise8(kx, kb);
+  const uint2 vc = quantise8(vx, vb);
+  if (!live) return;
+  uint4 qo;
+  qo.x = rope_rotate_pair(qv.x, m.cs[0]);
+  qo.y = rope_rotate_pair(qv.y, m.cs[1]);
+  qo.z = rope_rotate_pair(qv.z, m.cs[2]);
+  qo.w = rope_rotate_pair(qv.w, m.cs[3]);
+  *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(q.q_out) + m.e) = qo;
+  *reinterpret_cast<uint2 *>(static_cast<unsigned char *>(p.k_cache) + m.ce) = kc;
+  *reinterpret_cast<uint2 *>(static_cast<unsigned char *>(p.v_cache) + m.ce) = vc;
+  if ((threadIdx.x & 3) == 0) {
+    q.k_scale[m.ce / kQ8Block] = static_cast<unsigned char>(kb);
+    q.v_scale[m.ce / kQ8Block] = static_cast<unsigned char>(vb);
+  }
+}
+
+// Sixteen codes (half a block) a thread: 16 bytes in, 32 out.
+template <int D>
+__global__ void __launch_bounds__(kThreads) q8_cache_read_kernel(const Q8ReadParams p) {
+  constexpr int kVecs = D / 16;
+  const long long n = static_cast<long long>(p.n_rows) * kVecs;
+  for (long long head = blockIdx.y; head < p.heads; head += gridDim.y) {
+    for (long long it = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; it < n;
+         it += static_cast<long long>(gridDim.x) * kThreads) {
+      const int r = static_cast<int>(it / kVecs), c = static_cast<int>(it % kVecs);
+      const int row = r < p.seg_len[0] ? p.seg_row[0] + r : p.seg_row[1] + (r - p.seg_len[0]);
+      const long long src = (head * p.rows + row) * D + c * 16;
+      const long long dst = (head * p.n_rows + r) * D + c * 16;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        void *out = t ? p.v_out : p.k_out;
+        if (!out) continue;
+        const uint4 w = *reinterpret_cast<const uint4 *>((t ? p.v_cache : p.k_cache) + src);
+        const Q8Mul m = q8_mul((t ? p.v_scale : p.k_scale)[src / kQ8Block]);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint2 d = q8_decode4(u[i]);
+          o[2 * i] = bf16x2_mul(bf16x2_mul(d.x, m.m1), m.m2);
+          o[2 * i + 1] = bf16x2_mul(bf16x2_mul(d.y, m.m1), m.m2);
+        }
+        uint4 *d4 = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + dst);
+        d4[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        d4[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_q8_rope_kv_append(const Q8AppendParams &in, cudaStream_t stream) {
+  Q8AppendParams p = in;
+  RopeAppendParams &r = p.rope;
+  const long long n_items = static_cast<long long>(r.B) * r.L * r.H * (r.D / 8);
+  if (n_items < 1 || n_items >= (1ll << 31) - kThreads) return cudaErrorInvalidConfiguration;
+  r.slot0 = r.frame_idx % r.cap;
+  r.div_h = make_fastdiv(static_cast<uint32_t>(r.H));
+  r.div_l = make_fastdiv(static_cast<uint32_t>(r.L));
+  r.div_tf = make_fastdiv(static_cast<uint32_t>(r.Tf));
+  r.div_wg = make_fastdiv(static_cast<uint32_t>(r.Wg));
+  const unsigned blocks = static_cast<unsigned>((n_items + kThreads - 1) / kThreads);
+  const uint32_t n = static_cast<uint32_t>(n_items);
+  if (r.D == 128)
+    q8_rope_kv_append_kernel<128><<<blocks, kThreads, 0, stream>>>(p, n);
+  else if (r.D == 64)
+    q8_rope_kv_append_kernel<64><<<blocks, kThreads, 0, stream>>>(p, n);
+  else
+    return cudaErrorInvalidValue;
+  return cudaGetLastError();
+}
+
+cudaError_t launch_q8_cache_read(const Q8ReadParams &p, cudaStream_t stream) {
+  const long long n = static_cast<long long>(p.n_rows) * (p.D / 16);
+  const long long bx = (n + kThreads - 1) / kThreads;
+  const dim3 grid(static_cast<unsigned>(bx < (1ll << 30) ? bx : (1ll << 30)),
+                  static_cast<unsigned>(p.heads < 65535 ? p.heads : 65535));
+  if (p.D == 128)
+    q8_cache_read_kernel<128><<<grid, kThreads, 0, stream>>>(p);
+  else if (p.D == 64)
+    q8_cache_read_kernel<64><<<grid, kThreads, 0, stream>>>(p);
+  else
+    return cudaErrorInvalidValue;
+  return cudaGetLastError();
+}
+
+}  // namespace unstep

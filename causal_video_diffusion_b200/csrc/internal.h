@@ -88,6 +88,29 @@ struct RopeAppendParams {
 
 cudaError_t launch_rope_kv_append(const RopeAppendParams &p, cudaStream_t stream);
 
+// Append into an 8-bit cache: rope.q is read, q_out written; rope.k_cache and rope.v_cache hold
+// e4m3 codes, k_scale and v_scale a byte for every 32 of them.
+struct Q8AppendParams {
+  RopeAppendParams rope;
+  void *q_out;
+  unsigned char *k_scale, *v_scale;
+};
+
+cudaError_t launch_q8_rope_kv_append(const Q8AppendParams &p, cudaStream_t stream);
+
+// Rows of an 8-bit cache read back: output row r of a head is ring row seg_row[0] + r for
+// r < seg_len[0], then seg_row[1] + (r - seg_len[0]).
+struct Q8ReadParams {
+  const unsigned char *k_cache, *v_cache, *k_scale, *v_scale;
+  void *k_out, *v_out;  // bf16 [heads][n_rows][D]; either may be NULL
+  int heads, D;         // B * H
+  long long rows;       // cache rows per head
+  int n_rows;
+  int seg_row[2], seg_len[2];
+};
+
+cudaError_t launch_q8_cache_read(const Q8ReadParams &p, cudaStream_t stream);
+
 struct AttnParams {
   void *out;         // bf16 [act_B][L][act_H][D]; the shard's rows are written
   int *dev_error;
@@ -144,6 +167,15 @@ constexpr size_t attn_slot_floats(int D) { return 2 * (static_cast<size_t>(D) * 
 cudaError_t launch_window_attn(int D, const CUtensorMap &tmap_q, const CUtensorMap &tmap_k,
                                const CUtensorMap &tmap_v, const AttnParams &p,
                                cudaStream_t stream);
+
+// Attention over an 8-bit cache; D = head width.
+struct Q8AttnParams {
+  AttnParams attn;
+  const void *q;
+  const unsigned char *k_cache, *v_cache, *k_scale, *v_scale;
+};
+
+cudaError_t launch_q8_window_attn(int D, const Q8AttnParams &p, cudaStream_t stream);
 
 cudaError_t launch_wait_timeout_selftest(int *dev_error, uint64_t limit_ns, cudaStream_t stream);
 

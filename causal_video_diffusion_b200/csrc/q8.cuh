@@ -1,0 +1,76 @@
+// q8.cuh -- the 8-bit cache's number format: e4m3 codes under power-of-two scales, one scale for
+// 32 channels.
+//
+// A block with largest magnitude a has the exponent E = the smallest integer >= -111 with
+// a <= 448 * 2^E, held as the byte b = E + 127.  448 = 1.75 * 2^8, so with a = 2^e (1 + f), E is
+// e - 8 for f <= 0.75 and e - 7 above: on the bits of a, (bits + 0x1FFFFF) >> 23 carries into the
+// exponent field exactly when the 23-bit fraction exceeds 0x600000.  x / 2^E is exact (a power of
+// two), so the conversion to e4m3 is the only rounding.  E >= -111 keeps every non-zero stored
+// value at 2^-120 or above, a normal bf16 number.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include <cstdint>
+
+namespace unstep {
+
+constexpr int kQ8Block = 32;             // channels that share a scale
+constexpr int kQ8MinByte = 127 - 111;    // smallest scale byte of a block
+constexpr uint32_t kQ8NanByte = 255;     // a block with a NaN or an infinity
+constexpr uint32_t kQ8TopByte = 247;     // byte of blocks up to the largest fp32: codes up to 240
+
+// Scale byte of a block whose largest magnitude has the fp32 bits `abs_bits` (NaN and infinity
+// compare above every finite value).
+__device__ __forceinline__ uint32_t q8_scale_byte(uint32_t abs_bits) {
+  if (abs_bits >= 0x7F800000u) return kQ8NanByte;
+  const int b = static_cast<int>((abs_bits + 0x1FFFFFu) >> 23) - 8;
+  return static_cast<uint32_t>(max(b, kQ8MinByte));
+}
+
+// 1 / 2^E of a scale byte (bytes 16 .. 247; 0 for a NaN block, whose codes are zeros).
+__device__ __forceinline__ float q8_inv_scale(uint32_t byte) {
+  return byte == kQ8NanByte ? 0.f : __uint_as_float((254u - byte) << 23);
+}
+
+// Two values -> two codes (lo in the low byte).  lim is 448, or 240 under the top scale byte,
+// where 256 * 2^120 would already be infinite.
+__device__ __forceinline__ uint32_t q8_encode2(float lo, float hi, float inv, float lim) {
+  const float2 v = make_float2(fminf(fmaxf(lo * inv, -lim), lim), fminf(fmaxf(hi * inv, -lim), lim));
+  return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+}
+
+// bf16 pairs that multiply raw codes (see q8_decode2) up to their values: 2^(E + 120) as the
+// product m1 * m2, split because it exceeds bf16 for E > 7 (then m2 != 1).  A NaN block's m1 is NaN.
+struct Q8Mul {
+  uint32_t m1, m2;
+};
+
+__device__ __forceinline__ Q8Mul q8_mul(uint32_t byte) {
+  const uint32_t b1 = min(byte, 134u);
+  Q8Mul m;
+  m.m1 = byte == kQ8NanByte ? 0x7FC07FC0u : ((b1 + 120u) << 7) * 0x00010001u;
+  m.m2 = byte == kQ8NanByte ? 0x3F803F80u : ((byte - b1 + 127u) << 7) * 0x00010001u;
+  return m;
+}
+
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Two codes in bits 8-15 and 24-31 of w (other bits zero) -> a bf16 pair of their values times
+// 2^-120: sign to bit 15, the seven magnitude bits to bits 4-10 (e4m3's exponent bias is 7, bf16's
+// 127; subnormal codes become subnormal bf16 numbers of the same value).
+__device__ __forceinline__ uint32_t q8_decode2(uint32_t w) {
+  return (w & 0x80008000u) | ((w >> 4) & 0x07F007F0u);
+}
+
+// Four codes -> two bf16 pairs, times 2^-120.
+__device__ __forceinline__ uint2 q8_decode4(uint32_t c) {
+  return make_uint2(q8_decode2(__byte_perm(c, 0, 0x1404)), q8_decode2(__byte_perm(c, 0, 0x3424)));
+}
+
+}  // namespace unstep

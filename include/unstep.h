@@ -376,6 +376,137 @@ int unstep_cache_save(const unstep_cache_t *cache, void *host_dst, size_t bytes,
 int unstep_cache_restore(unstep_cache_t *cache, const void *host_src, size_t bytes,
                          unstep_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * 8-bit KV cache.  No counterpart in the paper: the ring cache of unstep_cache_t with K and V
+ * held in one byte per element, for windows (or numbers of layers and streams) whose bf16 cache
+ * does not fit, and for half the cache traffic.
+ *
+ * Every 32 consecutive channels of a K or V row share one power-of-two scale.  With a the largest
+ * magnitude of the block (K after its rotation, in fp32) and E the smallest integer >= -111 with
+ * a <= 448 * 2^E, an element x is held as the e4m3 number nearest to x / 2^E (round to nearest,
+ * ties to even: one rounding) and the block's scale as the byte E + 127.  A block that holds a
+ * NaN or an infinity gets the scale byte 255 and reads back as NaN throughout.  A block whose
+ * fp32 maximum is above 240 * 2^120 is held clamped to +-240 * 2^120, so that no finite input
+ * reads back as infinity.  Because the scales are powers of two, every stored value is exactly a
+ * bf16 number: reading the cache back and attending over it round nothing further.
+ *
+ * Layout: codes [B][H][cap_frames*Hg*Wg][D] bytes in base.k_cache and base.v_cache, scale bytes
+ * [B][H][cap_frames*Hg*Wg][D/32] in k_scale and v_scale, rows as in unstep_cache_t.
+ *
+ * The conventions at the top of this file hold.  unstep_append_plan, unstep_window_plan,
+ * unstep_cache_table_bytes, unstep_attn_scratch_bytes and unstep_get_device_error take &base; the
+ * calls that read or write bf16 rows refuse it with UNSTEP_ERR_ARG once the cache is initialised.
+ * ------------------------------------------------------------------------------------------ */
+typedef struct {
+  unstep_cache_t base; /* k_cache, v_cache: unstep_q8_cache_kv_bytes() bytes each */
+  void *k_scale;       /* unstep_q8_cache_scale_bytes() bytes, 16-byte aligned */
+  void *v_scale;
+} unstep_q8_cache_t;
+
+/* Bytes of ONE of base.k_cache / base.v_cache, and of ONE of k_scale / v_scale (0 if invalid). */
+size_t unstep_q8_cache_kv_bytes(const unstep_q8_cache_t *cache);
+size_t unstep_q8_cache_scale_bytes(const unstep_q8_cache_t *cache);
+
+/* unstep_cache_init for an 8-bit cache: the same checks, tables and metadata; zeroes codes and
+ * scales.  Errors: those of unstep_cache_init. */
+int unstep_q8_cache_init(unstep_q8_cache_t *cache, unstep_stream_t stream);
+
+/*
+ * unstep_rope_kv_append into an 8-bit cache: k is rotated and v copied, both are quantised as
+ * they are written.  The rotated queries go to q_out, bf16 in q's layout; q_out == q rotates in
+ * place, any other overlap is not allowed.  For a shard cache only the shard's streams and heads
+ * of q_out are written.  Frame order, slots and metadata as in unstep_rope_kv_append.
+ * Errors: those of unstep_rope_kv_append, plus UNSUPPORTED for 2^31 or more 8-channel vectors in
+ * the chunk.
+ */
+int unstep_q8_rope_kv_append(const void *q, void *q_out, const void *k, const void *v,
+                             unstep_q8_cache_t *cache, int frame_idx, unstep_grid_t grid,
+                             unstep_stream_t stream);
+
+/*
+ * unstep_window_attn over an 8-bit cache: softmax attention of the latest chunk's rotated queries
+ * over the stored values of the window's rows, bf16 tensor-core products with fp32 accumulation
+ * and fp32 online softmax, output rounded to bf16 (RNE).  Rows outside the window are not read.
+ * Errors: those of unstep_window_attn.
+ */
+int unstep_q8_window_attn(const void *q, const unstep_q8_cache_t *cache, int window, void *out,
+                          unstep_stream_t stream);
+
+/*
+ * Reads frames first_frame .. first_frame+frames-1 back, in time order, as bf16
+ * [B][H][frames*Hg*Wg][D] into k_out and v_out (either may be NULL, not both).  The values are
+ * exact (see above); K is the rotated K.  The frames must be in the ring: not before the stream's
+ * first frame, not after the newest one, and among the last cap_frames.
+ * Errors: ARG, ALIGN, WINDOW (a frame that the ring does not hold), CUDA.
+ */
+int unstep_q8_cache_read(const unstep_q8_cache_t *cache, int first_frame, int frames, void *k_out,
+                         void *v_out, unstep_stream_t stream);
+
+/*
+ * Checkpoint and resume of an 8-bit cache, as unstep_cache_save and unstep_cache_restore.  The
+ * buffer is theirs with magic "USTQ", followed after slot_frame by the K codes, the V codes, the
+ * K scales and the V scales.  Neither restore takes the other's buffer.
+ */
+size_t unstep_q8_cache_state_bytes(const unstep_q8_cache_t *cache);
+int unstep_q8_cache_save(const unstep_q8_cache_t *cache, void *host_dst, size_t bytes,
+                         unstep_stream_t stream);
+int unstep_q8_cache_restore(unstep_q8_cache_t *cache, const void *host_src, size_t bytes,
+                            unstep_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Norms before and after a DiT block, with its modulation, gate and residual.
+ * ------------------------------------------------------------------------------------------ */
+enum { UNSTEP_BF16 = 0, UNSTEP_F32 = 1 };        /* element types */
+enum { UNSTEP_NORM_LAYER = 0, UNSTEP_NORM_RMS = 1 };
+
+/*
+ * One norm over the C channels of a row, in fp32:
+ *   LAYER: n = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps)
+ *   RMS:   n = x / sqrt(mean(x^2) + eps)
+ *   result = (n * weight + bias) * (1 + scale_g) + shift_g
+ * weight and bias have C elements; scale_g and shift_g are group g's C elements, at element
+ * g * mod_stride of scale and shift.  Row r belongs to group r / rows_per_group (for a chunk:
+ * rows_per_group = Hg*Wg gives each frame a modulation of its own).  Each pointer may be NULL
+ * (left out); all have the element type param_type.
+ */
+typedef struct {
+  int kind;             /* UNSTEP_NORM_LAYER or UNSTEP_NORM_RMS */
+  float eps;            /* >= 0 */
+  int param_type;       /* UNSTEP_BF16 or UNSTEP_F32 */
+  const void *weight, *bias;
+  const void *scale, *shift;
+  long long mod_stride; /* elements between groups; used when scale or shift is given */
+} unstep_norm_t;
+
+/*
+ * y[r] = norm(x[r]) for r < rows: the norm and modulation before a block (or, with a weight
+ * alone, the norm of projected queries and keys).  x is bf16 or fp32 (x_type), y bf16 (RNE, one
+ * rounding).  Row strides ldx, ldy in elements, so x may be a column block of a wider tensor.
+ * C a multiple of 8, 8 <= C <= 16384; strides and mod_stride multiples of 8, ldx, ldy >= C when
+ * rows > 1; all pointers 16-byte aligned.  y may alias x when x is bf16 and ldy == ldx; no other
+ * overlap.  rows == 0 does nothing.
+ * Errors: ARG, SHAPE, ALIGN, UNSUPPORTED (C > 16384), CUDA.
+ */
+int unstep_norm_modulate(const void *x, int x_type, long long ldx, void *y, long long ldy,
+                         long long rows, int C, long long rows_per_group,
+                         const unstep_norm_t *norm, unstep_stream_t stream);
+
+/*
+ * The end of one block and the norm before the next, in one pass over the rows:
+ *   x_out[r] = x[r] + res_scale * gate_g * post(y[r])
+ *   h[r]     = next(x[r] + res_scale * gate_g * post(y[r]))      (from the fp32 sum, not x_out)
+ * x and x_out are bf16 or fp32 (x_type), y and h bf16.  gate: group g's C elements at element
+ * g * gate_stride, of type gate_type (NULL: 1).  post NULL: y itself.  next NULL: h is not
+ * computed (h must be NULL too).  x_out may be x itself with ldxo == ldx; no other overlap.
+ * Sizes, strides, groups, alignment and errors as in unstep_norm_modulate.
+ */
+int unstep_gate_residual_norm(const void *x, int x_type, long long ldx, const void *y,
+                              long long ldy, const void *gate, int gate_type,
+                              long long gate_stride, float res_scale, const unstep_norm_t *post,
+                              const unstep_norm_t *next, void *x_out, long long ldxo, void *h,
+                              long long ldh, long long rows, int C, long long rows_per_group,
+                              unstep_stream_t stream);
+
 /*
  * Synchronises `stream`, reads *cache->dev_error and returns it (UNSTEP_OK if no kernel reported
  * an error); CUDA if the copy or the synchronisation itself failed.
