@@ -18,7 +18,7 @@ LIB = os.path.join(PKG, "libunstep.so")
 # records UNSTEP_ERR_DEVICE_BOUNDS in the cache's error word instead of touching memory
 DEBUG_LIB = os.path.join(PKG, "libunstep_debug.so")
 SOURCES = ["api.cu", "rope_append.cu", "window_attn.cu", "lowrank_gemm.cu", "renoise.cu",
-           "conv3d.cu", "gemm2sm.cu", "cache_q8.cu", "window_attn_q8.cu", "block_norm.cu"]
+           "conv3d.cu", "gemm2sm.cu", "cache_q8.cu", "block_norm.cu"]
 HEADERS = ["internal.h", "limits.h", "gemm.h", "conv3d.h", "sm100.cuh", "rope_append.cuh", "q8.cuh",
            "block_norm.h"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

@@ -432,9 +432,11 @@ namespace {
 // the tensor maps, the persistent schedule and the launch.  `fixed_buffer` selects the scratch:
 // false, the cache's own (cache->attn_scratch, sized at unstep_cache_init; none: one CTA per
 // unit); true, the library's fixed device buffer, whose counters are zeroed on `st` first.
+// `q8`: the 8-bit cache whose base `cache` is, checked by the caller.
 int window_attn_launch(const void *q, const unstep_cache_t *cache, int window, void *out,
-                       unsigned flags, bool fixed_buffer, cudaStream_t st) {
-  int rc = check_ready(cache);
+                       unsigned flags, bool fixed_buffer, cudaStream_t st,
+                       const unstep_q8_cache_t *q8 = nullptr) {
+  int rc = q8 ? UNSTEP_OK : check_ready(cache);
   if (rc) return rc;
   if (flags & ~static_cast<unsigned>(UNSTEP_ATTN_ROPE_Q)) return UNSTEP_ERR_ARG;
   if (!q || !out) return UNSTEP_ERR_ARG;
@@ -484,7 +486,7 @@ int window_attn_launch(const void *q, const unstep_cache_t *cache, int window, v
     const cuuint32_t box[4] = {64, 1, 128, 1};
     if (!encode_bf16(&tq, q, 4, dims, str, box)) return UNSTEP_ERR_CUDA;
   }
-  {
+  if (!q8) {
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(R),
                                 static_cast<cuuint64_t>(B) * H};
     const cuuint64_t str[2] = {static_cast<cuuint64_t>(D) * 2,
@@ -566,7 +568,13 @@ int window_attn_launch(const void *q, const unstep_cache_t *cache, int window, v
     cudaGetLastError();
     return UNSTEP_ERR_CUDA;
   }
-  if (unstep::launch_window_attn(D, tq, tk, tv, p, st) != cudaSuccess) {
+  if (q8)
+    p.q8 = unstep::Q8Rows{static_cast<const unsigned char *>(cache->k_cache),
+                          static_cast<const unsigned char *>(cache->v_cache),
+                          static_cast<const unsigned char *>(q8->k_scale),
+                          static_cast<const unsigned char *>(q8->v_scale)};
+  if ((q8 ? unstep::launch_q8_window_attn(D, tq, p, st)
+          : unstep::launch_window_attn(D, tq, tk, tv, p, st)) != cudaSuccess) {
     cudaGetLastError();
     return UNSTEP_ERR_CUDA;
   }
@@ -884,43 +892,10 @@ int unstep_q8_rope_kv_append(const void *q, void *q_out, const void *k, const vo
 
 int unstep_q8_window_attn(const void *q, const unstep_q8_cache_t *cache, int window, void *out,
                           unstep_stream_t stream) {
-  int rc = check_ready_q8(cache);
+  const int rc = check_ready_q8(cache);
   if (rc) return rc;
-  if (!q || !out) return UNSTEP_ERR_ARG;
-  if (!aligned16(q) || !aligned16(out)) return UNSTEP_ERR_ALIGN;
-  const unstep_cache_t *c = &cache->base;
-  unstep_window_plan_t plan;
-  rc = unstep_window_plan(c, window, &plan);
-  if (rc) return rc;
-  unstep::Q8AttnParams p{};
-  unstep::AttnParams &a = p.attn;
-  a.out = out;
-  a.dev_error = c->dev_error;
-  a.B = c->B;
-  a.H = c->H;
-  a.act_H = act_H(c);
-  a.act_B = act_B(c);
-  a.b0 = c->b0;
-  a.h0 = c->h0;
-  a.L = c->last_chunk_frames * c->Hg * c->Wg;
-  a.rows = c->cap_frames * c->Hg * c->Wg;
-  for (int s = 0; s < 2; ++s) {
-    a.seg_row[s] = plan.seg_row[s];
-    a.seg_len[s] = plan.seg_len[s];
-  }
-  a.scale_log2 =
-      static_cast<float>(1.4426950408889634073599 / std::sqrt(static_cast<double>(c->D)));
-  p.q = q;
-  p.k_cache = static_cast<const unsigned char *>(c->k_cache);
-  p.v_cache = static_cast<const unsigned char *>(c->v_cache);
-  p.k_scale = static_cast<const unsigned char *>(cache->k_scale);
-  p.v_scale = static_cast<const unsigned char *>(cache->v_scale);
-  if (unstep::launch_q8_window_attn(c->D, p, reinterpret_cast<cudaStream_t>(stream)) !=
-      cudaSuccess) {
-    cudaGetLastError();
-    return UNSTEP_ERR_CUDA;
-  }
-  return UNSTEP_OK;
+  return window_attn_launch(q, &cache->base, window, out, 0u, false,
+                            reinterpret_cast<cudaStream_t>(stream), cache);
 }
 
 int unstep_q8_cache_read(const unstep_q8_cache_t *cache, int first_frame, int frames, void *k_out,

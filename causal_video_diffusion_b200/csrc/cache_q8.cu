@@ -112,14 +112,20 @@ __global__ void __launch_bounds__(kThreads) q8_cache_read_kernel(const Q8ReadPar
         void *out = t ? p.v_out : p.k_out;
         if (!out) continue;
         const uint4 w = *reinterpret_cast<const uint4 *>((t ? p.v_cache : p.k_cache) + src);
-        const Q8Mul m = q8_mul((t ? p.v_scale : p.k_scale)[src / kQ8Block]);
+        const uint32_t byte = (t ? p.v_scale : p.k_scale)[src / kQ8Block];
+        const uint32_t m1 = q8_mul1(byte);
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
         uint32_t o[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint2 d = q8_decode4(u[i]);
-          o[2 * i] = bf16x2_mul(bf16x2_mul(d.x, m.m1), m.m2);
-          o[2 * i + 1] = bf16x2_mul(bf16x2_mul(d.y, m.m1), m.m2);
+          o[2 * i] = bf16x2_mul(d.x, m1);
+          o[2 * i + 1] = bf16x2_mul(d.y, m1);
+        }
+        if (byte > kQ8SplitByte) {
+          const uint32_t m2 = q8_mul2(byte);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = bf16x2_mul(o[i], m2);
         }
         uint4 *d4 = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + dst);
         d4[0] = make_uint4(o[0], o[1], o[2], o[3]);

@@ -111,6 +111,11 @@ struct Q8ReadParams {
 
 cudaError_t launch_q8_cache_read(const Q8ReadParams &p, cudaStream_t stream);
 
+// Rows of an 8-bit cache: e4m3 codes [B*H][rows][D] and a scale byte for every 32 of them.
+struct Q8Rows {
+  const unsigned char *k_codes, *v_codes, *k_scale, *v_scale;
+};
+
 struct AttnParams {
   void *out;         // bf16 [act_B][L][act_H][D]; the shard's rows are written
   int *dev_error;
@@ -149,6 +154,7 @@ struct AttnParams {
   int tab_smem;      // 1: the chunk's rows fit in kQRopeTabBytes and are staged in shared memory
   FastDiv div_tf;    // by Tf
   FastDiv div_wg;    // by Wg
+  Q8Rows q8;         // launch_q8_window_attn's K and V
 };
 
 // Shared memory for the coefficient rows of the query rotation: frames*d_t/2 + Hg*d_h/2 +
@@ -168,14 +174,9 @@ cudaError_t launch_window_attn(int D, const CUtensorMap &tmap_q, const CUtensorM
                                const CUtensorMap &tmap_v, const AttnParams &p,
                                cudaStream_t stream);
 
-// Attention over an 8-bit cache; D = head width.
-struct Q8AttnParams {
-  AttnParams attn;
-  const void *q;
-  const unsigned char *k_cache, *v_cache, *k_scale, *v_scale;
-};
-
-cudaError_t launch_q8_window_attn(int D, const Q8AttnParams &p, cudaStream_t stream);
+// The same over an 8-bit cache (p.q8).
+cudaError_t launch_q8_window_attn(int D, const CUtensorMap &tmap_q, const AttnParams &p,
+                                  cudaStream_t stream);
 
 cudaError_t launch_wait_timeout_selftest(int *dev_error, uint64_t limit_ns, cudaStream_t stream);
 

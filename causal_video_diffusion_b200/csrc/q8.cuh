@@ -42,17 +42,16 @@ __device__ __forceinline__ uint32_t q8_encode2(float lo, float hi, float inv, fl
 }
 
 // bf16 pairs that multiply raw codes (see q8_decode2) up to their values: 2^(E + 120) as the
-// product m1 * m2, split because it exceeds bf16 for E > 7 (then m2 != 1).  A NaN block's m1 is NaN.
-struct Q8Mul {
-  uint32_t m1, m2;
-};
+// product of two, because it exceeds bf16 for E > 7; the second, needed for bytes above
+// kQ8SplitByte alone, is NaN for a NaN block.
+constexpr uint32_t kQ8SplitByte = 134;
 
-__device__ __forceinline__ Q8Mul q8_mul(uint32_t byte) {
-  const uint32_t b1 = min(byte, 134u);
-  Q8Mul m;
-  m.m1 = byte == kQ8NanByte ? 0x7FC07FC0u : ((b1 + 120u) << 7) * 0x00010001u;
-  m.m2 = byte == kQ8NanByte ? 0x3F803F80u : ((byte - b1 + 127u) << 7) * 0x00010001u;
-  return m;
+__device__ __forceinline__ uint32_t q8_mul1(uint32_t byte) {
+  return (min(byte, kQ8SplitByte) + 120u) * 0x00800080u;
+}
+
+__device__ __forceinline__ uint32_t q8_mul2(uint32_t byte) {
+  return byte == kQ8NanByte ? 0x7FC07FC0u : (byte - kQ8SplitByte + 127u) * 0x00800080u;
 }
 
 __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {

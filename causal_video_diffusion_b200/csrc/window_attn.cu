@@ -29,6 +29,13 @@
 // by more than 8 (log2 units): below that, P <= 2^8 is exact enough in bf16/fp32 and O needs no
 // rescale; above it, the owning warp rescales its O rows in TMEM after the previous PV retired.
 //
+// Over an 8-bit cache (kQ8; 512 threads) K and V arrive as e4m3 codes under a power-of-two scale
+// per 32 channels, half the bytes, and every value is exactly a bf16 number.  Warps 12-15 read a
+// key tile's codes into registers (the next half tile's loads in flight while this one's are
+// decoded: about 2.5 instructions an element), write it as bf16 into the stage that the TMA would
+// have filled, and announce it; rows behind the segment's end become zeros.  Everything behind the
+// stage is the bf16 kernel's.  A score that is not finite makes its query row NaN.
+//
 // Every wait is bounded (WaitGuard): on a timeout the CTA records UNSTEP_ERR_DEVICE_TIMEOUT,
 // lets in-flight TMA copies and MMAs land, frees TMEM and exits.
 #include <cuda_bf16.h>
@@ -37,12 +44,13 @@
 
 #include "../../include/unstep.h"
 #include "internal.h"
+#include "q8.cuh"
 #include "sm100.cuh"
 
 namespace unstep {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreadsBf16 = 384;
 // Register split: launched at 168 per thread (384 x 168 = 64512), the producer/MMA warpgroup
 // drops to kRegsIo and the two softmax warpgroups rise to kRegsSoftmax; the static_assert keeps
 // 2 x 128 x kRegsSoftmax + 128 x kRegsIo within the launch total (184/128: 63488), so the claim
@@ -56,7 +64,13 @@ constexpr int kThreads = 384;
 #endif
 constexpr int kRegsSoftmax = UNSTEP_REGS_SOFTMAX;
 constexpr int kRegsIo = UNSTEP_REGS_IO;
-static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsIo <= kThreads * 168, "register split");
+static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsIo <= kThreadsBf16 * 168, "register split");
+// Over an 8-bit cache a fourth warpgroup decodes K and V.  Launched at 128 per thread (512 x 128 =
+// 65536): softmax 184, producer/MMA 64, decoding 80 add up to exactly that.
+constexpr int kThreadsQ8 = 512;
+constexpr int kRegsIoQ8 = 64, kRegsDecode = 80;
+static_assert(2 * 128 * kRegsSoftmax + 128 * (kRegsIoQ8 + kRegsDecode) <= kThreadsQ8 * 128,
+              "register split");
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr uint64_t kDrainLimitNs = 1000000000ull;
 
@@ -64,8 +78,9 @@ constexpr uint64_t kDrainLimitNs = 1000000000ull;
 #define UNSTEP_KV_STAGES 2
 #endif
 
-template <int D, bool kRopeQ = false>
+template <int D, bool kRopeQ, bool kQ8>
 struct Cfg {
+  static constexpr int kThreads = kQ8 ? kThreadsQ8 : kThreadsBf16;
   static constexpr int kBoxes = D / 64;                // 128-byte swizzle boxes per row
   static constexpr int kTileBytes = 128 * D * 2;       // 128 rows x D bf16
   static constexpr int kStages = UNSTEP_KV_STAGES;     // ring stages, one key tile's K and V each
@@ -123,20 +138,24 @@ __device__ __forceinline__ void wait_drain(uint64_t *bar, uint32_t parity) {
 #endif
 constexpr int kEmuPairsPer8 = UNSTEP_EMU_PAIRS_PER8;
 
-// Max of a row's 128 scores: eight independent chains of 3-input max, then a short tree.
+// Max of a row's 128 scores: eight independent chains of 3-input max, then a short tree.  kNan: NaN
+// if one of them is.
+template <bool kNan>
 __device__ __forceinline__ float row_max128(const uint32_t (&s)[4][32]) {
+  auto max3 = [](float a, float b, float c) { return kNan ? fmax3_nan(a, b, c) : fmax3(a, b, c); };
+  auto max2 = [](float a, float b) { return kNan ? fmax3_nan(a, b, b) : fmaxf(a, b); };
   float m8[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const int c = k >> 1, e0 = (k & 1) * 16;
-    float m = fmax3(__uint_as_float(s[c][e0]), __uint_as_float(s[c][e0 + 1]),
-                    __uint_as_float(s[c][e0 + 2]));
+    float m = max3(__uint_as_float(s[c][e0]), __uint_as_float(s[c][e0 + 1]),
+                   __uint_as_float(s[c][e0 + 2]));
 #pragma unroll
     for (int e = 3; e < 15; e += 2)
-      m = fmax3(m, __uint_as_float(s[c][e0 + e]), __uint_as_float(s[c][e0 + e + 1]));
-    m8[k] = fmaxf(m, __uint_as_float(s[c][e0 + 15]));
+      m = max3(m, __uint_as_float(s[c][e0 + e]), __uint_as_float(s[c][e0 + e + 1]));
+    m8[k] = max2(m, __uint_as_float(s[c][e0 + 15]));
   }
-  return fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+  return max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]), max2(m8[6], m8[7]));
 }
 
 // P for one 32-column chunk of a row: p = 2^(s * scale - m), summed into acc (four packed
@@ -447,13 +466,66 @@ UNSTEP_COLD_FN void merge_row(const AttnParams &p, int i, int row, long long t0,
   }
 }
 
+// This decoding thread's part of one half tile (the K or the V rows of a key tile): kSteps vectors
+// of 16 codes and their scale bytes.  Thread t takes channels 16 (t mod D/16) .. of rows
+// t / (D/16) + i * kRowStep, so its swizzle phase (row mod 8) never changes.
+template <int D>
+struct HalfTile {
+  static constexpr int kVecs = D / 16, kRowStep = 128 / kVecs, kSteps = kVecs;
+  uint4 w[kSteps];
+  uint32_t byte[kSteps];
+
+  // Vector i of the tile whose first row is cache row `row0` (of all heads' rows); rows from
+  // `valid` on are zeros.
+  __device__ __forceinline__ void load(int i, const unsigned char *codes,
+                                       const unsigned char *scales, long long row0, int valid,
+                                       int t) {
+    const int r = t / kVecs + i * kRowStep, c = t % kVecs;
+    w[i] = make_uint4(0, 0, 0, 0);
+    byte[i] = 127;
+    if (r < valid) {
+      const long long row = row0 + r;
+      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                   : "l"(codes + row * D + c * 16));
+      byte[i] = __ldg(scales + row * (D / kQ8Block) + c / 2);
+    }
+  }
+
+  // Vector i decoded into the 128-byte-swizzled bf16 tile: two 16-byte chunks.  The lanes of a
+  // row's upper box store their chunks in the other order, so that eight lanes hit eight chunks.
+  __device__ __forceinline__ void store(int i, uint8_t *tile, int t) const {
+    const int r = t / kVecs + i * kRowStep, c = t % kVecs;
+    const uint32_t m1 = q8_mul1(byte[i]);
+    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    uint32_t o[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint2 d = q8_decode4(u[e]);
+      o[2 * e] = bf16x2_mul(d.x, m1);
+      o[2 * e + 1] = bf16x2_mul(d.y, m1);
+    }
+    if (byte[i] > kQ8SplitByte) {
+      const uint32_t m2 = q8_mul2(byte[i]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = bf16x2_mul(o[e], m2);
+    }
+    uint8_t *dst = tile + (c >> 2) * 16384 + r * 128;
+    const int ch = (c & 3) * 2, swap = c >> 2;
+    const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+    *reinterpret_cast<uint4 *>(dst + (((ch + swap) ^ (r & 7)) << 4)) = swap ? hi : lo;
+    *reinterpret_cast<uint4 *>(dst + (((ch + 1 - swap) ^ (r & 7)) << 4)) = swap ? lo : hi;
+  }
+};
+
 // kRopeQ: q is un-rotated; both softmax warpgroups rotate their query tiles in shared memory.
-template <int D, bool kRopeQ>
-__global__ void __launch_bounds__(kThreads, 1)
+// kQ8: the cache is an 8-bit one (p.q8), decoded by a fourth warpgroup; tmk and tmv are not used.
+template <int D, bool kRopeQ, bool kQ8>
+__global__ void __launch_bounds__((Cfg<D, kRopeQ, kQ8>::kThreads), 1)
     window_attn_kernel(const __grid_constant__ CUtensorMap tmq,
                        const __grid_constant__ CUtensorMap tmk,
                        const __grid_constant__ CUtensorMap tmv, const AttnParams p) {
-  using C = Cfg<D, kRopeQ>;
+  using C = Cfg<D, kRopeQ, kQ8>;
   constexpr int NS = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -480,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], kQ8 ? 128 : 1);
       mbar_init(&empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -505,14 +577,75 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int E = UNSTEP_ERR_DEVICE_TIMEOUT;
   const SkRange sk = sk_range(p, cta);
 
-  if (warp >= 8) {
-    regs_release<kRegsIo>();
+  if (kQ8 && warp >= 12) {
+    if constexpr (kQ8) {
+      regs_release<kRegsDecode>();
+      // ------------------------------------------------------------ K and V decoding
+      const int t = threadIdx.x & 127;
+      const auto *kc = p.q8.k_codes, *vc = p.q8.v_codes, *ks = p.q8.k_scale, *vs = p.q8.v_scale;
+      HalfTile<D> h;
+      Seg sg{};
+      long long head_row = 0, row0 = 0;
+      int q = 0, kt = 0, valid = 0;
+      bool more = get_seg(p, cta, sk, 0, sg);
+      auto locate = [&] {
+        int row;
+        key_tile(p, kt, row, valid);
+        row0 = head_row + row;
+        if (kDebugChecks && !debug_check(kt >= 0 && kt < p.n_tiles && row >= 0 && valid >= 1 &&
+                                             row + min(valid, 128) <= p.rows && row0 >= 0 &&
+                                             row0 < static_cast<long long>(p.B) * p.H * p.rows,
+                                         p.dev_error)) {
+          *abort_flag = 1;
+          valid = 0;
+        }
+      };
+      auto enter = [&] {
+        head_row = static_cast<long long>(unit_pos(p, sg.u).bh) * p.rows;
+        kt = sg.k0;
+        locate();
+      };
+      if (more) {
+        enter();
+#pragma unroll
+        for (int i = 0; i < h.kSteps; ++i) h.load(i, kc, ks, row0, valid, t);
+      }
+      for (int n = 0; more; ++n) {
+        const int s = n % NS;
+        const uint32_t r = static_cast<uint32_t>(n / NS);
+        if (!__all_sync(kFull, wait_bounded(&empty[s], (r & 1u) ^ 1u, g, E))) break;
+        uint8_t *st = smem + C::kSmemKV + s * C::kStageBytes;
+#pragma unroll
+        for (int i = 0; i < h.kSteps; ++i) {
+          h.store(i, st, t);
+          h.load(i, vc, vs, row0, valid, t);
+        }
+        if (++kt < sg.k1) {
+          locate();
+        } else if ((more = get_seg(p, cta, sk, ++q, sg))) {
+          enter();
+        } else {
+          valid = 0;   // nothing follows: the loads below read nothing
+        }
+#pragma unroll
+        for (int i = 0; i < h.kSteps; ++i) {
+          h.store(i, st + C::kTileBytes, t);
+          h.load(i, kc, ks, row0, valid, t);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&full[s]);
+      }
+    }
+  } else if (warp >= 8) {
+    regs_release<kQ8 ? kRegsIoQ8 : kRegsIo>();
     if (warp == 8) {
       // -------------------------------------------------------------- TMA producer
       if (lane == 0) {
         tma_prefetch_desc(&tmq);
-        tma_prefetch_desc(&tmk);
-        tma_prefetch_desc(&tmv);
+        if constexpr (!kQ8) {
+          tma_prefetch_desc(&tmk);
+          tma_prefetch_desc(&tmv);
+        }
         int n = 0;   // key tiles (K/V stages) issued
         int nq = 0;  // Q loads issued
         bool ok = true;
@@ -537,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_4d(smem + C::kSmemQ + t * C::kTileBytes + c * 16384, &tmq, q_full,
                           c * 64, p.h0 + up.h, up.q0 + t * 128, p.b0 + up.b);
           nq = q + 1;
-          for (int kt = sg.k0; ok && kt < sg.k1; ++kt) {
+          for (int kt = sg.k0; !kQ8 && ok && kt < sg.k1; ++kt) {
             int row, valid;
             key_tile(p, kt, row, valid);
             if (kDebugChecks &&
@@ -740,11 +873,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 32; ++e)
               if (c * 32 + e >= valid) s[c][e] = __float_as_uint(-INFINITY);
         }
-        const float mt = row_max128(s) * scale;
+        float mt = row_max128<kQ8>(s) * scale;
+        if constexpr (kQ8) {
+          // a row with a NaN or infinite maximum is NaN from here on (the exponentials on the FMA
+          // pipe would lose a NaN); one with nothing but -inf so far keeps its sum at zero
+          mt = mt < INFINITY ? fmaxf(mt, -3.0e38f) : __uint_as_float(0x7FC00000u);
+        }
         if (j == 0) {
           m_run = mt;
-        } else if (__any_sync(kFull, mt > m_run + 8.f)) {
-          const float m_new = fmaxf(m_run, mt);
+        } else if (__any_sync(kFull, kQ8 ? !(mt <= m_run + 8.f) : mt > m_run + 8.f)) {
+          const float m_new = kQ8 ? fmax3_nan(m_run, mt, mt) : fmaxf(m_run, mt);
           const float f = ex2_approx(m_run - m_new);
           l_run *= f;
           m_run = m_new;
@@ -875,10 +1013,10 @@ __global__ void exp2_selftest_kernel(const float *x, float *y_poly, float *y_muf
   }
 }
 
-template <int D, bool kRopeQ>
+template <int D, bool kRopeQ, bool kQ8>
 cudaError_t launch_d(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                      const AttnParams &p, cudaStream_t stream) {
-  using C = Cfg<D, kRopeQ>;
+  using C = Cfg<D, kRopeQ, kQ8>;
   // the shared-memory opt-in is per device; remember which devices have it
   static unsigned long long attr_set = 0;
   int dev = 0;
@@ -886,14 +1024,14 @@ cudaError_t launch_d(const CUtensorMap &tq, const CUtensorMap &tk, const CUtenso
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (dev >= 64 || !(__atomic_load_n(&attr_set, __ATOMIC_ACQUIRE) & bit)) {
-    e = cudaFuncSetAttribute(window_attn_kernel<D, kRopeQ>,
+    e = cudaFuncSetAttribute(window_attn_kernel<D, kRopeQ, kQ8>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemAlloc);
     if (e != cudaSuccess) return e;
     if (dev < 64) __atomic_fetch_or(&attr_set, bit, __ATOMIC_RELEASE);
   }
   if (p.grid < 1) return cudaErrorInvalidConfiguration;
-  window_attn_kernel<D, kRopeQ>
-      <<<static_cast<unsigned>(p.grid), kThreads, C::kSmemAlloc, stream>>>(tq, tk, tv, p);
+  window_attn_kernel<D, kRopeQ, kQ8>
+      <<<static_cast<unsigned>(p.grid), C::kThreads, C::kSmemAlloc, stream>>>(tq, tk, tv, p);
   return cudaGetLastError();
 }
 
@@ -903,11 +1041,18 @@ cudaError_t launch_window_attn(int D, const CUtensorMap &tmap_q, const CUtensorM
                                const CUtensorMap &tmap_v, const AttnParams &p,
                                cudaStream_t stream) {
   if (D == 128)
-    return p.rope_q ? launch_d<128, true>(tmap_q, tmap_k, tmap_v, p, stream)
-                    : launch_d<128, false>(tmap_q, tmap_k, tmap_v, p, stream);
+    return p.rope_q ? launch_d<128, true, false>(tmap_q, tmap_k, tmap_v, p, stream)
+                    : launch_d<128, false, false>(tmap_q, tmap_k, tmap_v, p, stream);
   if (D == 64)
-    return p.rope_q ? launch_d<64, true>(tmap_q, tmap_k, tmap_v, p, stream)
-                    : launch_d<64, false>(tmap_q, tmap_k, tmap_v, p, stream);
+    return p.rope_q ? launch_d<64, true, false>(tmap_q, tmap_k, tmap_v, p, stream)
+                    : launch_d<64, false, false>(tmap_q, tmap_k, tmap_v, p, stream);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_q8_window_attn(int D, const CUtensorMap &tmap_q, const AttnParams &p,
+                                  cudaStream_t stream) {
+  if (D == 128) return launch_d<128, false, true>(tmap_q, tmap_q, tmap_q, p, stream);
+  if (D == 64) return launch_d<64, false, true>(tmap_q, tmap_q, tmap_q, p, stream);
   return cudaErrorInvalidValue;
 }
 
