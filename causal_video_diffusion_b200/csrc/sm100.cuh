@@ -303,13 +303,6 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return d;
 }
 
-// The same, NaN if an operand is.
-__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
 // Packed pairs of fp32 values (low, high) for the sm_100 f32x2 arithmetic.
 __device__ __forceinline__ uint64_t f2_make(float lo, float hi) {
   uint64_t r;

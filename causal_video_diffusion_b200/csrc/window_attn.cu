@@ -30,11 +30,11 @@
 // rescale; above it, the owning warp rescales its O rows in TMEM after the previous PV retired.
 //
 // Over an 8-bit cache (kQ8; 512 threads) K and V arrive as e4m3 codes under a power-of-two scale
-// per 32 channels, half the bytes, and every value is exactly a bf16 number.  Warps 12-15 read a
-// key tile's codes into registers (the next half tile's loads in flight while this one's are
-// decoded: about 2.5 instructions an element), write it as bf16 into the stage that the TMA would
-// have filled, and announce it; rows behind the segment's end become zeros.  Everything behind the
-// stage is the bf16 kernel's.  A score that is not finite makes its query row NaN.
+// per 32 channels, half the bytes, and every value is exactly a bf16 number.  Warps 12-15 copy a
+// key tile's codes into shared memory (cp.async, one tile ahead), decode them (about 2.5
+// instructions an element), write the tile as bf16 into the stage that the TMA would have filled,
+// and announce it; rows behind the segment's end become zeros.  Everything behind the stage is the
+// bf16 kernel's.
 //
 // Every wait is bounded (WaitGuard): on a timeout the CTA records UNSTEP_ERR_DEVICE_TIMEOUT,
 // lets in-flight TMA copies and MMAs land, frees TMEM and exits.
@@ -66,9 +66,10 @@ constexpr int kRegsSoftmax = UNSTEP_REGS_SOFTMAX;
 constexpr int kRegsIo = UNSTEP_REGS_IO;
 static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsIo <= kThreadsBf16 * 168, "register split");
 // Over an 8-bit cache a fourth warpgroup decodes K and V.  Launched at 128 per thread (512 x 128 =
-// 65536): softmax 184, producer/MMA 64, decoding 80 add up to exactly that.
+// 65536): softmax 184, producer/MMA 88, decoding 56 add up to exactly that (88/56 measured 3 %
+// faster than 72/72).
 constexpr int kThreadsQ8 = 512;
-constexpr int kRegsIoQ8 = 64, kRegsDecode = 80;
+constexpr int kRegsIoQ8 = 88, kRegsDecode = 56;
 static_assert(2 * 128 * kRegsSoftmax + 128 * (kRegsIoQ8 + kRegsDecode) <= kThreadsQ8 * 128,
               "register split");
 constexpr uint32_t kFull = 0xFFFFFFFFu;
@@ -87,7 +88,8 @@ struct Cfg {
   static constexpr int kStageBytes = 2 * kTileBytes;   // K tile, then V tile
   static constexpr int kSmemQ = 0;
   static constexpr int kSmemKV = 2 * kTileBytes;
-  static constexpr int kSmemBar = kSmemKV + kStages * kStageBytes;
+  static constexpr int kSmemCodes = kSmemKV + kStages * kStageBytes;  // one key tile's codes (kQ8)
+  static constexpr int kSmemBar = kSmemCodes + (kQ8 ? 2 * 128 * D : 0);
   static constexpr int kSmemTab = kSmemBar + 256;      // RoPE rows of the chunk (kRopeQ)
   static constexpr int kSmemUsed = kSmemTab + (kRopeQ ? kQRopeTabBytes : 0);
   // at least ~116 KB so that a second CTA (which would block on TMEM) never shares the SM
@@ -137,32 +139,31 @@ __device__ __forceinline__ void wait_drain(uint64_t *bar, uint32_t parity) {
 #define UNSTEP_EMU_PAIRS_PER8 2
 #endif
 constexpr int kEmuPairsPer8 = UNSTEP_EMU_PAIRS_PER8;
+// Over an 8-bit cache none: the decoding warps need the FMA and ALU issue slots and the instruction
+// cache more (12 heads, 4680 queries, 32760 keys: 0.97 ms against 1.00 and 1.02 with 1 and 2 of 8).
+// MUFU also turns a score that is not finite into a NaN row, which the polynomial would not.
 
-// Max of a row's 128 scores: eight independent chains of 3-input max, then a short tree.  kNan: NaN
-// if one of them is.
-template <bool kNan>
+// Max of a row's 128 scores: eight independent chains of 3-input max, then a short tree.
 __device__ __forceinline__ float row_max128(const uint32_t (&s)[4][32]) {
-  auto max3 = [](float a, float b, float c) { return kNan ? fmax3_nan(a, b, c) : fmax3(a, b, c); };
-  auto max2 = [](float a, float b) { return kNan ? fmax3_nan(a, b, b) : fmaxf(a, b); };
   float m8[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const int c = k >> 1, e0 = (k & 1) * 16;
-    float m = max3(__uint_as_float(s[c][e0]), __uint_as_float(s[c][e0 + 1]),
-                   __uint_as_float(s[c][e0 + 2]));
+    float m = fmax3(__uint_as_float(s[c][e0]), __uint_as_float(s[c][e0 + 1]),
+                    __uint_as_float(s[c][e0 + 2]));
 #pragma unroll
     for (int e = 3; e < 15; e += 2)
-      m = max3(m, __uint_as_float(s[c][e0 + e]), __uint_as_float(s[c][e0 + e + 1]));
-    m8[k] = max2(m, __uint_as_float(s[c][e0 + 15]));
+      m = fmax3(m, __uint_as_float(s[c][e0 + e]), __uint_as_float(s[c][e0 + e + 1]));
+    m8[k] = fmaxf(m, __uint_as_float(s[c][e0 + 15]));
   }
-  return max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]), max2(m8[6], m8[7]));
+  return fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
 }
 
 // P for one 32-column chunk of a row: p = 2^(s * scale - m), summed into acc (four packed
 // accumulators), rounded to bf16 pairs and stored to the 16 TMEM columns at `taddr` (for
 // D = 128 the P columns alias the S columns already read).  kMasked: columns >= valid are zero (a segment's
 // last, partial tile), all exponentials on MUFU so that masked ones are exactly 0.
-template <bool kMasked>
+template <bool kMasked, int kEmu>
 __device__ __forceinline__ void exp_chunk(const uint32_t (&s)[32], int col0, int valid,
                                           uint64_t sc2, uint64_t nm2, uint64_t (&acc)[4],
                                           uint32_t taddr) {
@@ -173,7 +174,7 @@ __device__ __forceinline__ void exp_chunk(const uint32_t (&s)[32], int col0, int
     const uint64_t x2 = ffma2(f2_make(__uint_as_float(s[2 * pi]), __uint_as_float(s[2 * pi + 1])),
                               sc2, nm2);
     uint64_t p2;
-    if (!kMasked && (pi & 7) >= 8 - kEmuPairsPer8) {
+    if (!kMasked && (pi & 7) >= 8 - kEmu) {
       p2 = exp2_poly2(x2);
     } else {
       float x0, x1;
@@ -466,55 +467,106 @@ UNSTEP_COLD_FN void merge_row(const AttnParams &p, int i, int row, long long t0,
   }
 }
 
-// This decoding thread's part of one half tile (the K or the V rows of a key tile): kSteps vectors
-// of 16 codes and their scale bytes.  Thread t takes channels 16 (t mod D/16) .. of rows
-// t / (D/16) + i * kRowStep, so its swizzle phase (row mod 8) never changes.
+// A decoding thread's part of a half tile (the K or the V rows of a key tile): kSteps vectors of 16
+// codes, copied into slots of shared memory that only this thread uses (so its own wait for its
+// copies is all the synchronisation they need).  Step i is box (64 channels) i mod kBoxes of rows
+// 32 (i / kBoxes) ..; thread t takes its row t / 4 and channels 16 (t mod 4) ..: eight lanes store
+// to eight different chunks of the swizzled tile.  A warp's rows are 32 in all: lane l loads the
+// scales of its row l, and a step takes them by a shuffle.
+// The loop over the steps is rolled: a half tile decoded in straight-line code ran at 5.5 clocks
+// an instruction, its 17 KB and the softmax's putting each other out of the instruction cache.
 template <int D>
-struct HalfTile {
-  static constexpr int kVecs = D / 16, kRowStep = 128 / kVecs, kSteps = kVecs;
-  uint4 w[kSteps];
-  uint32_t byte[kSteps];
+struct Decoder {
+  static constexpr int kBoxes = D / 64, kSteps = 4 * kBoxes, kScales = D / kQ8Block;
+  int t, row, srow;   // row within a tile of step 0; row whose scales this lane loads
+  uint32_t slot;      // shared-memory address of this thread's vector 0 (K's; V's follow)
+  uint32_t d0, d1;    // where the two chunks of vector 0 go in stage 0's K tile
 
-  // Vector i of the tile whose first row is cache row `row0` (of all heads' rows); rows from
-  // `valid` on are zeros.
-  __device__ __forceinline__ void load(int i, const unsigned char *codes,
-                                       const unsigned char *scales, long long row0, int valid,
-                                       int t) {
-    const int r = t / kVecs + i * kRowStep, c = t % kVecs;
-    w[i] = make_uint4(0, 0, 0, 0);
-    byte[i] = 127;
-    if (r < valid) {
-      const long long row = row0 + r;
-      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
-                   : "l"(codes + row * D + c * 16));
-      byte[i] = __ldg(scales + row * (D / kQ8Block) + c / 2);
-    }
+  __device__ __forceinline__ Decoder(int thread, const void *slots, const void *stages) {
+    t = thread;
+    row = t >> 2;
+    srow = ((t & 31) >> 3) * 32 + (t >> 5) * 8 + (t & 7);
+    slot = smem_u32(slots) + t * 16;
+    const int c = (t & 3) * 2, x = row & 7;
+    d0 = smem_u32(stages) + row * 128 + ((c ^ x) << 4);
+    d1 = smem_u32(stages) + row * 128 + (((c + 1) ^ x) << 4);
   }
 
-  // Vector i decoded into the 128-byte-swizzled bf16 tile: two 16-byte chunks.  The lanes of a
-  // row's upper box store their chunks in the other order, so that eight lanes hit eight chunks.
-  __device__ __forceinline__ void store(int i, uint8_t *tile, int t) const {
-    const int r = t / kVecs + i * kRowStep, c = t % kVecs;
-    const uint32_t m1 = q8_mul1(byte[i]);
-    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-    uint32_t o[8];
+  // Starts the copy of step i's vector; rows from `valid` on become zeros.  src: the tile's codes.
+  __device__ __forceinline__ void fetch(int i, uint32_t at, const unsigned char *src,
+                                        int valid) const {
+    const int r = i / kBoxes * 32 + row;
+    if (r < valid)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at),
+                   "l"(src + r * D + i % kBoxes * 64 + (t & 3) * 16)
+                   : "memory");
+    else
+      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+  }
+
+  // Scale bytes of this lane's row.  src: the tile's scales.
+  __device__ __forceinline__ uint32_t scales(const unsigned char *src, int valid) const {
+    if (srow >= valid) return 0x7F7F7F7Fu;
+    return D == 128 ? __ldg(reinterpret_cast<const uint32_t *>(src + srow * kScales))
+                    : __ldg(reinterpret_cast<const uint16_t *>(src + srow * kScales));
+  }
+
+  __device__ __forceinline__ void start(int half, const unsigned char *src, int valid) const {
+#pragma unroll 1
+    for (int i = 0; i < kSteps; ++i) fetch(i, slot + half * (128 * D) + i * 2048, src, valid);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+
+  // Decodes half tile `half` under the scales `word` into the swizzled bf16 tile `tile` bytes
+  // behind stage 0's K tile, starting the copies of the next one (src, valid) as it goes.
+  __device__ __forceinline__ void decode(int half, uint32_t word, uint32_t tile,
+                                         const unsigned char *src, int valid) const {
+    constexpr int kU = 4;  // steps a turn: 2 measured 1-3 % slower
+    uint32_t at = slot + half * (128 * D), to = tile;
+#pragma unroll 1
+    for (int i0 = 0; i0 < kSteps; i0 += kU, at += 2048 * kU, to += 4096 * kU / kBoxes) {
+      uint32_t u[kU][4], byte[kU], o[kU][8], top = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint2 d = q8_decode4(u[e]);
-      o[2 * e] = bf16x2_mul(d.x, m1);
-      o[2 * e + 1] = bf16x2_mul(d.y, m1);
-    }
-    if (byte[i] > kQ8SplitByte) {
-      const uint32_t m2 = q8_mul2(byte[i]);
+      for (int k = 0; k < kU; ++k)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(u[k][0]), "=r"(u[k][1]), "=r"(u[k][2]), "=r"(u[k][3])
+                     : "r"(at + k * 2048));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = bf16x2_mul(o[e], m2);
+      for (int k = 0; k < kU; ++k) {
+        const int i = i0 + k;
+        const uint32_t w = __shfl_sync(kFull, word, i / kBoxes * 8 + ((t & 31) >> 2));
+        byte[k] = (w >> ((t & 2) * 4 + i % kBoxes * 16)) & 0xFFu;
+        top = max(top, byte[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < kU; ++k) {
+        const uint32_t m1 = q8_mul1(byte[k]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint2 d = q8_decode4(u[k][e]);
+          o[k][2 * e] = bf16x2_mul(d.x, m1);
+          o[k][2 * e + 1] = bf16x2_mul(d.y, m1);
+        }
+      }
+      if (top > kQ8SplitByte) {
+#pragma unroll
+        for (int k = 0; k < kU; ++k)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[k][e] = bf16x2_mul(o[k][e], q8_mul2(byte[k]));
+      }
+#pragma unroll
+      for (int k = 0; k < kU; ++k) {
+        const uint32_t b = to + (k % kBoxes) * 16384 + k / kBoxes * 4096;
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(d0 + b), "r"(o[k][0]),
+                     "r"(o[k][1]), "r"(o[k][2]), "r"(o[k][3])
+                     : "memory");
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(d1 + b), "r"(o[k][4]),
+                     "r"(o[k][5]), "r"(o[k][6]), "r"(o[k][7])
+                     : "memory");
+        fetch(i0 + k, at + k * 2048, src, valid);
+      }
     }
-    uint8_t *dst = tile + (c >> 2) * 16384 + r * 128;
-    const int ch = (c & 3) * 2, swap = c >> 2;
-    const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-    *reinterpret_cast<uint4 *>(dst + (((ch + swap) ^ (r & 7)) << 4)) = swap ? hi : lo;
-    *reinterpret_cast<uint4 *>(dst + (((ch + 1 - swap) ^ (r & 7)) << 4)) = swap ? lo : hi;
+    asm volatile("cp.async.commit_group;" ::: "memory");
   }
 };
 
@@ -540,7 +592,11 @@ __global__ void __launch_bounds__((Cfg<D, kRopeQ, kQ8>::kThreads), 1)
   uint64_t *o_done = p_ready + 2;
   uint64_t *drain = o_done + 2;
   uint64_t *q_rot = drain + 1;    // query tiles rotated by both warpgroups (kRopeQ)
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(q_rot + 1);
+  // kQ8: a stage's K and V tiles apart, `full` and `empty` being K's first and V's second; K's is
+  // free a period before V's, time that the decoding needs
+  uint64_t *k_empty = q_rot + 1;
+  uint64_t *v_full = k_empty + (kQ8 ? NS : 0);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(v_full + (kQ8 ? NS : 0));
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   volatile int *merge_word = reinterpret_cast<volatile int *>(tmem_slot + 2);  // [2]
 
@@ -554,6 +610,10 @@ __global__ void __launch_bounds__((Cfg<D, kRopeQ, kQ8>::kThreads), 1)
     for (int s = 0; s < NS; ++s) {
       mbar_init(&full[s], kQ8 ? 128 : 1);
       mbar_init(&empty[s], 1);
+      if constexpr (kQ8) {
+        mbar_init(&k_empty[s], 1);
+        mbar_init(&v_full[s], 128);
+      }
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
@@ -581,13 +641,12 @@ __global__ void __launch_bounds__((Cfg<D, kRopeQ, kQ8>::kThreads), 1)
     if constexpr (kQ8) {
       regs_release<kRegsDecode>();
       // ------------------------------------------------------------ K and V decoding
-      const int t = threadIdx.x & 127;
-      const auto *kc = p.q8.k_codes, *vc = p.q8.v_codes, *ks = p.q8.k_scale, *vs = p.q8.v_scale;
-      HalfTile<D> h;
+      const Decoder<D> dec(threadIdx.x & 127, smem + C::kSmemCodes, smem + C::kSmemKV);
+      constexpr int kSc = Decoder<D>::kScales;
       Seg sg{};
       long long head_row = 0, row0 = 0;
       int q = 0, kt = 0, valid = 0;
-      bool more = get_seg(p, cta, sk, 0, sg);
+      bool more = get_seg(p, cta, sk, 0, sg), ok = true;
       auto locate = [&] {
         int row;
         key_tile(p, kt, row, valid);
@@ -605,36 +664,41 @@ __global__ void __launch_bounds__((Cfg<D, kRopeQ, kQ8>::kThreads), 1)
         kt = sg.k0;
         locate();
       };
+      uint32_t word[2];
       if (more) {
         enter();
-#pragma unroll
-        for (int i = 0; i < h.kSteps; ++i) h.load(i, kc, ks, row0, valid, t);
+        dec.start(0, p.q8.k_codes + row0 * D, valid);
+        dec.start(1, p.q8.v_codes + row0 * D, valid);
+        word[0] = dec.scales(p.q8.k_scale + row0 * kSc, valid);
+        word[1] = dec.scales(p.q8.v_scale + row0 * kSc, valid);
       }
-      for (int n = 0; more; ++n) {
+      for (int n = 0; more && ok; ++n) {
         const int s = n % NS;
-        const uint32_t r = static_cast<uint32_t>(n / NS);
-        if (!__all_sync(kFull, wait_bounded(&empty[s], (r & 1u) ^ 1u, g, E))) break;
-        uint8_t *st = smem + C::kSmemKV + s * C::kStageBytes;
-#pragma unroll
-        for (int i = 0; i < h.kSteps; ++i) {
-          h.store(i, st, t);
-          h.load(i, vc, vs, row0, valid, t);
-        }
+        const uint32_t par = (static_cast<uint32_t>(n / NS) & 1u) ^ 1u;
+        // the next tile's copies start as this one's slots are read
         if (++kt < sg.k1) {
           locate();
         } else if ((more = get_seg(p, cta, sk, ++q, sg))) {
           enter();
         } else {
-          valid = 0;   // nothing follows: the loads below read nothing
+          valid = 0;   // nothing follows
         }
-#pragma unroll
-        for (int i = 0; i < h.kSteps; ++i) {
-          h.store(i, st + C::kTileBytes, t);
-          h.load(i, kc, ks, row0, valid, t);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          ok = __all_sync(kFull, wait_bounded(half ? &empty[s] : &k_empty[s], par, g, E));
+          if (!ok) break;
+          const uint32_t next =
+              dec.scales((half ? p.q8.v_scale : p.q8.k_scale) + row0 * kSc, valid);
+          asm volatile("cp.async.wait_group 1;" ::: "memory");  // the other half's may be open
+          dec.decode(half, word[0], static_cast<uint32_t>(s * C::kStageBytes + half * C::kTileBytes),
+                     (half ? p.q8.v_codes : p.q8.k_codes) + row0 * D, valid);
+          word[0] = word[1];
+          word[1] = next;
+          fence_proxy_async_smem();
+          mbar_arrive(half ? &v_full[s] : &full[s]);
         }
-        fence_proxy_async_smem();
-        mbar_arrive(&full[s]);
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else if (warp >= 8) {
     regs_release<kQ8 ? kRegsIoQ8 : kRegsIo>();
@@ -758,10 +822,15 @@ __global__ void __launch_bounds__((Cfg<D, kRopeQ, kQ8>::kThreads), 1)
             qk(1, n % NS);
             umma_commit(&s_full[1]);
           }
+          if constexpr (kQ8) umma_commit(&k_empty[n % NS]);
           if (ntl == 1) umma_commit(q_empty);
           for (int j = 0; j < ntl; ++j) {
             const int st = (n + j) % NS, nst = (n + j + 1) % NS;
             const bool more = j + 1 < ntl;
+            if constexpr (kQ8) {
+              if (!(ok = wait_bounded(&v_full[st], static_cast<uint32_t>((n + j) / NS) & 1u, g, E)))
+                break;
+            }
             if (!(ok = wait_bounded(&p_ready[0], done0 & 1u, g, E))) break;
             tc_fence_after();
             pv(0, st, j > 0);
@@ -786,6 +855,7 @@ __global__ void __launch_bounds__((Cfg<D, kRopeQ, kQ8>::kThreads), 1)
                 qk(1, nst);
                 umma_commit(&s_full[1]);
               }
+              if constexpr (kQ8) umma_commit(&k_empty[nst]);
               if (j + 2 == ntl) umma_commit(q_empty);  // the segment's last QK^T is issued
             }
           }
@@ -809,6 +879,7 @@ __global__ void __launch_bounds__((Cfg<D, kRopeQ, kQ8>::kThreads), 1)
     const uint32_t tO = tmem + lane_base + (i ? C::kTmO1 : C::kTmO0);
     const float scale = p.scale_log2;
     constexpr int kTileFloats = D * 128 + 256;  // one query tile of a scratch slot
+    constexpr int kEmu = kQ8 ? 0 : kEmuPairsPer8;
     uint32_t cnt = 0;                           // key tiles this warpgroup has processed
     uint32_t n_seg = 0;                         // segments of this query tile completed
     bool ok = true;
@@ -873,16 +944,13 @@ __global__ void __launch_bounds__((Cfg<D, kRopeQ, kQ8>::kThreads), 1)
             for (int e = 0; e < 32; ++e)
               if (c * 32 + e >= valid) s[c][e] = __float_as_uint(-INFINITY);
         }
-        float mt = row_max128<kQ8>(s) * scale;
-        if constexpr (kQ8) {
-          // a row with a NaN or infinite maximum is NaN from here on (the exponentials on the FMA
-          // pipe would lose a NaN); one with nothing but -inf so far keeps its sum at zero
-          mt = mt < INFINITY ? fmaxf(mt, -3.0e38f) : __uint_as_float(0x7FC00000u);
-        }
+        float mt = row_max128(s) * scale;
+        // kQ8: a tile of nothing but -inf leaves the sum at zero instead of making it NaN
+        if constexpr (kQ8) mt = fmaxf(mt, -3.0e38f);
         if (j == 0) {
           m_run = mt;
-        } else if (__any_sync(kFull, kQ8 ? !(mt <= m_run + 8.f) : mt > m_run + 8.f)) {
-          const float m_new = kQ8 ? fmax3_nan(m_run, mt, mt) : fmaxf(m_run, mt);
+        } else if (__any_sync(kFull, mt > m_run + 8.f)) {
+          const float m_new = fmaxf(m_run, mt);
           const float f = ex2_approx(m_run - m_new);
           l_run *= f;
           m_run = m_new;
@@ -901,14 +969,14 @@ __global__ void __launch_bounds__((Cfg<D, kRopeQ, kQ8>::kThreads), 1)
         const uint64_t sc2 = f2_make(scale, scale);
         const uint64_t nm2 = f2_make(-m_run, -m_run);
         uint64_t acc[4] = {0, 0, 0, 0};
-        if (!masked) {
+        if (kQ8 || !masked) {   // MUFU makes the masked columns' -inf exactly 0
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            exp_chunk<false>(s[c], c * 32, 128, sc2, nm2, acc, tP + c * 16);
+            exp_chunk<false, kEmu>(s[c], c * 32, 128, sc2, nm2, acc, tP + c * 16);
         } else {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            exp_chunk<true>(s[c], c * 32, valid, sc2, nm2, acc, tP + c * 16);
+            exp_chunk<true, kEmu>(s[c], c * 32, valid, sc2, nm2, acc, tP + c * 16);
         }
         float a0, a1;
         f2_split(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), a0, a1);
