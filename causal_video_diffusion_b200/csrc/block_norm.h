@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/unstep.h"
+#include "internal.h"
 
 namespace unstep {
 
@@ -20,6 +21,10 @@ struct NormParams {
   int has_post;
   float res_scale;
   unstep_norm_t post, next;
+  // set by launch_block_norm: rows and groups below 2^31, division by rows_per_group, every fp32
+  // pointer on 32 bytes (row and group strides are multiples of 8 elements)
+  bool narrow, wide;
+  FastDiv div_group;
 };
 
 // gated = false: h = next(x).  gated = true: x_out = x + res_scale * gate * post(y), h = next of it.
