@@ -6,7 +6,6 @@ library's kernels.  There is no fallback: if the library cannot be loaded, every
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import NamedTuple, Optional, Tuple
@@ -426,26 +425,41 @@ class LayerCache:
         return out_h
 
 
-def _on(device: torch.device, stream: Optional[torch.cuda.Stream]):
-    """(stream handle on `device`, guard that makes `device` current for the call)."""
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    guard = _SAME_DEVICE if torch.cuda.current_device() == device.index else \
-        torch.cuda.device(device)
-    return int(s.cuda_stream), guard
+# The 8-bit cache's and the norms' calls take a few microseconds of host time, as long as their
+# kernels do for small chunks, so their checks use what torch answers fastest: the device's index
+# and the current stream's handle without the objects around them.
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
-_SAME_DEVICE = contextlib.nullcontext()
+def _call(fn, name: str, index: int, stream: Optional[torch.cuda.Stream], args: tuple) -> None:
+    """``fn(*args, stream handle)`` with device `index` current; `stream` None: its current one."""
+    if stream is None:
+        handle = _current_stream(index)
+    elif stream.device_index != index:
+        raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on cuda:{index}")
+    else:
+        handle = stream.cuda_stream
+    if _current_device() == index:
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, handle)
+    if rc < 0:
+        raise UnstepError(rc, name)
 
 
-def _new_on(stream: Optional[torch.cuda.Stream], shape, dtype, device) -> torch.Tensor:
-    """An output that a call on `stream` writes: its memory is not reused before the stream is
-    done with it."""
-    t = torch.empty(shape, dtype=dtype, device=device)
+def _new_like(t: torch.Tensor, dtype: torch.dtype,
+              stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """A contiguous output of t's shape that a call on `stream` writes: its memory is not reused
+    before the stream is done with it."""
+    if t.dtype is dtype:
+        out = torch.empty_like(t, memory_format=torch.contiguous_format)
+    else:
+        out = torch.empty(t.shape, dtype=dtype, device=t.device)
     if stream is not None:
-        t.record_stream(stream)
-    return t
+        out.record_stream(stream)
+    return out
 
 
 class LayerCacheQ8(LayerCache):
@@ -478,10 +492,20 @@ class LayerCacheQ8(LayerCache):
 
     def reset(self, stream: Optional[torch.cuda.Stream] = None) -> None:
         """Back to an empty cache, as after construction."""
-        handle, guard = _on(self.device, stream)
-        with guard:
-            _check(lib().unstep_q8_cache_init(ctypes.byref(self.q8), handle),
-                   "unstep_q8_cache_init")
+        self._ref = ctypes.byref(self.q8)
+        self._index = self.k_codes.get_device()
+        self._rows_like = {}     # frames -> a one-element tensor expanded to read_frames' shape
+        _call(lib().unstep_q8_cache_init, "unstep_q8_cache_init", self._index, stream,
+              (self._ref,))
+
+    def _act(self, t: torch.Tensor, frames: int, name: str) -> int:
+        """Address of a checked activation tensor of `frames` frames."""
+        c = self.c
+        if (t.dtype is torch.bfloat16 and t.get_device() == self._index and t.is_contiguous()
+                and t.shape == (self.act_B, frames * self.Tf, self.act_H, c.D)):
+            return t.data_ptr()
+        self._check_act(t, self.chunk_len(frames), name)
+        raise ValueError(f"{name} must be contiguous")
 
     def rope_kv_append(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, frame_idx: int,
                        frames: int, stream: Optional[torch.cuda.Stream] = None,
@@ -491,16 +515,16 @@ class LayerCacheQ8(LayerCache):
         Returns the rotated q."""
         if defer_q:
             raise ValueError("an 8-bit cache rotates the queries in the append (no defer_q)")
-        q_out = q if q_out is None else q_out
-        L = self.chunk_len(frames)
-        for t, n in ((q, "q"), (k, "k"), (v, "v"), (q_out, "q_out")):
-            self._check_act(t, L, n)
-        handle, guard = _on(self.device, stream)
-        with guard:
-            _check(lib().unstep_q8_rope_kv_append(
-                _dev_ptr(q, "q"), _dev_ptr(q_out, "q_out"), _dev_ptr(k, "k"), _dev_ptr(v, "v"),
-                ctypes.byref(self.q8), int(frame_idx),
-                unstep_grid_t(frames, self.c.Hg, self.c.Wg), handle), "unstep_q8_rope_kv_append")
+        qp = self._act(q, frames, "q")
+        kp, vp = self._act(k, frames, "k"), self._act(v, frames, "v")
+        op = qp
+        if q_out is None:
+            q_out = q
+        else:
+            op = self._act(q_out, frames, "q_out")
+        _call(lib().unstep_q8_rope_kv_append, "unstep_q8_rope_kv_append", self._index, stream,
+              (qp, op, kp, vp, self._ref, int(frame_idx),
+               unstep_grid_t(frames, self.c.Hg, self.c.Wg)))
         return q_out
 
     def window_attn(self, q: torch.Tensor, window: int, out: Optional[torch.Tensor] = None,
@@ -509,16 +533,12 @@ class LayerCacheQ8(LayerCache):
         """Attention of the latest chunk's rotated queries over the last ``window`` frames."""
         if rope_q:
             raise ValueError("an 8-bit cache takes rotated queries (no rope_q)")
-        L = self.chunk_len(self.c.last_chunk_frames)
-        self._check_act(q, L, "q")
+        frames = self.c.last_chunk_frames
+        qp = self._act(q, frames, "q")
         if out is None:
-            out = _new_on(stream, q.shape, q.dtype, q.device)
-        self._check_act(out, L, "out")
-        handle, guard = _on(self.device, stream)
-        with guard:
-            _check(lib().unstep_q8_window_attn(_dev_ptr(q, "q"), ctypes.byref(self.q8),
-                                               int(window), _dev_ptr(out, "out"), handle),
-                   "unstep_q8_window_attn")
+            out = _new_like(q, torch.bfloat16, stream)
+        _call(lib().unstep_q8_window_attn, "unstep_q8_window_attn", self._index, stream,
+              (qp, self._ref, int(window), self._act(out, frames, "out")))
         return out
 
     def read_frames(self, first_frame: int, frames: int, k_out: Optional[torch.Tensor] = None,
@@ -527,24 +547,29 @@ class LayerCacheQ8(LayerCache):
                     ) -> Tuple[torch.Tensor, torch.Tensor]:
         """K (rotated) and V of frames ``first_frame .. first_frame+frames-1`` in time order, as
         bf16 ``[B][H][frames*Tf][D]``.  The ring must hold the frames."""
-        c = self.c
-        if frames < 1 or frames > c.cap_frames:
-            raise UnstepError(UNSTEP_ERR_WINDOW if frames > 0 else UNSTEP_ERR_ARG, "read_frames")
-        want = (c.B, c.H, frames * self.Tf, c.D)
-        outs = []
-        for t, n in ((k_out, "k_out"), (v_out, "v_out")):
-            if t is None:
-                t = _new_on(stream, want, torch.bfloat16, self.device)
-            elif t.dtype != torch.bfloat16 or tuple(t.shape) != want or t.device != self.device:
-                raise ValueError(f"{n} must be bfloat16 {want} on {self.device}")
-            outs.append(t)
-        handle, guard = _on(self.device, stream)
-        with guard:
-            _check(lib().unstep_q8_cache_read(ctypes.byref(self.q8), int(first_frame),
-                                              int(frames), _dev_ptr(outs[0], "k_out"),
-                                              _dev_ptr(outs[1], "v_out"), handle),
-                   "unstep_q8_cache_read")
-        return outs[0], outs[1]
+        like = self._rows_like.get(frames)
+        if like is None:
+            c = self.c
+            if frames < 1 or frames > c.cap_frames:
+                raise UnstepError(UNSTEP_ERR_WINDOW if frames > 0 else UNSTEP_ERR_ARG, "read_frames")
+            like = torch.empty(1, dtype=torch.bfloat16, device=self.device)
+            like = like.expand(c.B, c.H, frames * self.Tf, c.D)
+            self._rows_like[frames] = like
+        k_out = self._rows_out(k_out, like, "k_out", stream)
+        v_out = self._rows_out(v_out, like, "v_out", stream)
+        _call(lib().unstep_q8_cache_read, "unstep_q8_cache_read", self._index, stream,
+              (self._ref, int(first_frame), frames, k_out.data_ptr(), v_out.data_ptr()))
+        return k_out, v_out
+
+    def _rows_out(self, t: Optional[torch.Tensor], like: torch.Tensor, name: str,
+                  stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+        if t is None:
+            return _new_like(like, torch.bfloat16, stream)
+        if t.dtype is not torch.bfloat16 or t.shape != like.shape or \
+                t.get_device() != self._index or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous bfloat16 {tuple(like.shape)} on "
+                             f"{self.device}")
+        return t
 
     def state_bytes(self) -> int:
         return lib().unstep_q8_cache_state_bytes(ctypes.byref(self.q8))
@@ -769,73 +794,97 @@ _TYPES = {torch.bfloat16: UNSTEP_BF16, torch.float32: UNSTEP_F32}
 def _rows_of(t: torch.Tensor, name: str) -> Tuple[int, int]:
     """(rows, row stride) of a tensor whose last axis is contiguous and whose leading axes walk
     its rows at one stride."""
-    shape, strides = t.shape, t.stride()
-    if len(shape) < 2:
+    shape = t.shape
+    n = len(shape)
+    if n < 2:
         raise ValueError(f"{name} must have a row axis and a channel axis")
-    if shape[-1] > 1 and strides[-1] != 1:
+    C = shape[-1]
+    if n == 2:
+        rows = shape[0]
+        ld, st = t.stride()
+        if rows <= 1 or C == 0:
+            ld = C if rows <= 1 else ld
+            rows = rows if C else 0
+    else:
+        strides = t.stride()
+        st, rows, ld = strides[-1], 1, C
+        if t.numel() == 0:
+            return 0, C
+        for m, s in zip(reversed(shape[:-1]), reversed(strides[:-1])):
+            if m != 1:
+                if rows == 1:
+                    ld = s
+                elif s != ld * rows:
+                    raise ValueError(f"{name}'s rows must lie at one stride")
+                rows *= m
+    if C > 1 and st != 1:
         raise ValueError(f"{name}'s channels must be contiguous")
-    if t.numel() == 0:
-        return 0, shape[-1]
-    rows, ld = 1, shape[-1]
-    for n, st in zip(reversed(shape[:-1]), reversed(strides[:-1])):
-        if n != 1:
-            if rows == 1:
-                ld = st
-            elif st != ld * rows:
-                raise ValueError(f"{name}'s rows must lie at one stride")
-        rows *= n
-    if ld < shape[-1]:
+    if ld < C:
         raise ValueError(f"{name}'s rows must not overlap")
     return rows, ld
 
 
-def _vectors(t: Optional[torch.Tensor], C: int, groups: Optional[int], rows: int, name: str,
-             dev: torch.device) -> Tuple[Optional[int], int, Optional[int]]:
-    """(pointer, group stride, groups) of a [G][C] modulation tensor."""
-    if t is None:
-        return None, 0, groups
-    if t.dim() != 2 or t.shape[1] != C or t.stride(1) != 1 or t.device != dev or \
-            t.dtype not in _TYPES:
-        raise ValueError(f"{name} must be bf16 or fp32 [groups][{C}] on {dev}, channels contiguous")
-    G = t.shape[0]
-    if G < 1 or rows % G or (groups is not None and groups != G):
+def _vectors(t: torch.Tensor, C: int, groups: int, rows: int, name: str,
+             index: int) -> Tuple[int, int, int]:
+    """(pointer, group stride, groups) of a [G][C] modulation tensor; groups 0: not yet known."""
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != C or t.get_device() != index or t.dtype not in _TYPES:
+        raise ValueError(f"{name} must be bf16 or fp32 [groups][{C}] on cuda:{index}")
+    G = shape[0]
+    ld, st = t.stride()
+    if st != 1:
+        raise ValueError(f"{name}'s channels must be contiguous")
+    if G < 1 or rows % G or (groups and groups != G):
         raise ValueError(f"{name} has {G} groups for {rows} rows"
-                         + ("" if groups is None else f", other modulations {groups}"))
-    return t.data_ptr(), (t.stride(0) if G > 1 else 0), G
+                         + (f", other modulations {groups}" if groups else ""))
+    return t.data_ptr(), (ld if G > 1 else 0), G
 
 
-def _norm_struct(n: Norm, C: int, rows: int, groups: Optional[int], dev: torch.device):
+def _norm_struct(n: Norm, C: int, rows: int, groups: int, index: int):
     """(unstep_norm_t, groups) of a Norm for `rows` rows of C channels."""
-    kind = _NORM_KINDS.get(n.kind)
-    if kind is None:
-        raise ValueError(f"norm kind {n.kind!r}: 'layer' or 'rms'")
-    types = {t.dtype for t in n[2:] if t is not None}
-    if len(types) > 1 or not types <= _TYPES.keys():
-        raise ValueError("a norm's weight, bias, scale and shift must be all bf16 or all fp32")
-    s = unstep_norm_t()
-    s.kind, s.eps = kind, n.eps
-    s.param_type = _TYPES[types.pop()] if types else UNSTEP_F32
-    for name in ("weight", "bias"):
-        t = getattr(n, name)
-        if t is not None:
-            if t.shape != (C,) or not t.is_contiguous() or t.device != dev:
-                raise ValueError(f"{name} must be contiguous [{C}] on {dev}")
-            setattr(s, name, t.data_ptr())
-    s.scale, ld, groups = _vectors(n.scale, C, groups, rows, "scale", dev)
-    s.shift, ld2, groups = _vectors(n.shift, C, groups, rows, "shift", dev)
-    if n.scale is not None and n.shift is not None and ld != ld2:
-        raise ValueError("scale and shift must have the same row stride")
-    s.mod_stride = ld or ld2
-    return s, groups
+    kind, eps, weight, bias, scale, shift = n
+    code = _NORM_KINDS.get(kind)
+    if code is None:
+        raise ValueError(f"norm kind {kind!r}: 'layer' or 'rms'")
+    dtype = wp = bp = cp = hp = None
+    ld = ld2 = 0
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is None:
+            continue
+        if t.shape != (C,) or t.get_device() != index or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous [{C}] on cuda:{index}")
+        if name == "weight":
+            wp, dtype = t.data_ptr(), t.dtype
+        else:
+            bp = t.data_ptr()
+            if dtype is None:
+                dtype = t.dtype
+    if scale is not None:
+        cp, ld, groups = _vectors(scale, C, groups, rows, "scale", index)
+        if dtype is None:
+            dtype = scale.dtype
+    if shift is not None:
+        hp, ld2, groups = _vectors(shift, C, groups, rows, "shift", index)
+        if dtype is None:
+            dtype = shift.dtype
+        if scale is not None and ld != ld2:
+            raise ValueError("scale and shift must have the same row stride")
+    ptype = UNSTEP_F32
+    if dtype is not None:
+        ptype = _TYPES.get(dtype, -1)
+        if ptype < 0 or (bias is not None and bias.dtype is not dtype) or \
+                (scale is not None and scale.dtype is not dtype) or \
+                (shift is not None and shift.dtype is not dtype):
+            raise ValueError("a norm's weight, bias, scale and shift must be all bf16 or all fp32")
+    return unstep_norm_t(code, eps, ptype, wp, bp, cp, hp, ld or ld2), groups
 
 
 def _norm_out(t: Optional[torch.Tensor], like: torch.Tensor, dtype: torch.dtype, name: str,
               stream: Optional[torch.cuda.Stream]) -> Tuple[torch.Tensor, int]:
     """(output, row stride): `t` checked against `like`, or a new contiguous tensor."""
     if t is None:
-        t = _new_on(stream, like.shape, dtype, like.device)
-        return t, like.shape[-1]
-    if t.shape != like.shape or t.dtype != dtype or t.device != like.device:
+        return _new_like(like, dtype, stream), like.shape[-1]
+    if t.dtype is not dtype or t.shape != like.shape or t.get_device() != like.get_device():
         raise ValueError(f"{name} must be {dtype} {tuple(like.shape)} on {like.device}")
     return t, _rows_of(t, name)[1]
 
@@ -847,17 +896,16 @@ def norm_modulate(x: torch.Tensor, norm: Norm, out: Optional[torch.Tensor] = Non
     The norm and modulation before a DiT block, or with a weight alone the norm of projected
     queries and keys.  ``out`` may be x itself when x is bf16.
     """
-    if not x.is_cuda or x.dtype not in _TYPES:
+    xt, index = _TYPES.get(x.dtype, -1), x.get_device()
+    if xt < 0 or index < 0:
         raise ValueError("x must be a bf16 or fp32 CUDA tensor")
     rows, ldx = _rows_of(x, "x")
     C = x.shape[-1]
-    spec, groups = _norm_struct(norm, C, rows, None, x.device)
+    spec, groups = _norm_struct(norm, C, rows, 0, index)
     out, ldo = _norm_out(out, x, torch.bfloat16, "out", stream)
-    handle, guard = _on(x.device, stream)
-    with guard:
-        _check(lib().unstep_norm_modulate(x.data_ptr(), _TYPES[x.dtype], ldx, out.data_ptr(), ldo,
-                                          rows, C, max(1, rows // (groups or 1)),
-                                          ctypes.byref(spec), handle), "unstep_norm_modulate")
+    _call(lib().unstep_norm_modulate, "unstep_norm_modulate", index, stream,
+          (x.data_ptr(), xt, ldx, out.data_ptr(), ldo, rows, C,
+           (rows // groups if groups else rows) or 1, ctypes.byref(spec)))
     return out
 
 
@@ -875,34 +923,39 @@ def gate_residual_norm(x: torch.Tensor, y: torch.Tensor, gate: Optional[torch.Te
     ``next`` None leaves the second output out (None).  ``next`` sees the fp32 sum, before it is
     rounded to x's type.  Returns (x_out, out).
     """
-    if not x.is_cuda or x.dtype not in _TYPES:
+    xt, index = _TYPES.get(x.dtype, -1), x.get_device()
+    if xt < 0 or index < 0:
         raise ValueError("x must be a bf16 or fp32 CUDA tensor")
-    if y.dtype != torch.bfloat16 or y.shape != x.shape or y.device != x.device:
+    if y.dtype is not torch.bfloat16 or y.shape != x.shape or y.get_device() != index:
         raise ValueError(f"y must be bfloat16 {tuple(x.shape)} on {x.device}")
     rows, ldx = _rows_of(x, "x")
     ldy = _rows_of(y, "y")[1]
-    C, dev = x.shape[-1], x.device
-    gp, gs, groups = _vectors(gate, C, None, rows, "gate", dev)
-    post_s = next_s = None
+    C = x.shape[-1]
+    gp, gt, gs, groups = None, UNSTEP_F32, 0, 0
+    if gate is not None:
+        gp, gs, groups = _vectors(gate, C, 0, rows, "gate", index)
+        gt = _TYPES[gate.dtype]
+    pr = nr = op = None
+    ldo = 0
     if post is not None:
-        post_s, groups = _norm_struct(post, C, rows, groups, dev)
+        spec, groups = _norm_struct(post, C, rows, groups, index)
+        pr = ctypes.byref(spec)
     if next is not None:
-        next_s, groups = _norm_struct(next, C, rows, groups, dev)
+        spec, groups = _norm_struct(next, C, rows, groups, index)
+        nr = ctypes.byref(spec)
     elif out is not None:
         raise ValueError("out without a next norm")
-    x_out, ldxo = (x, ldx) if x_out is None else _norm_out(x_out, x, x.dtype, "x_out", stream)
-    op, ldo = None, 0
+    ldxo = ldx
+    if x_out is None:
+        x_out = x
+    else:
+        x_out, ldxo = _norm_out(x_out, x, x.dtype, "x_out", stream)
     if next is not None:
         out, ldo = _norm_out(out, x, torch.bfloat16, "out", stream)
         op = out.data_ptr()
-    handle, guard = _on(dev, stream)
-    with guard:
-        _check(lib().unstep_gate_residual_norm(
-            x.data_ptr(), _TYPES[x.dtype], ldx, y.data_ptr(), ldy, gp,
-            UNSTEP_F32 if gate is None else _TYPES[gate.dtype], gs, float(res_scale),
-            None if post_s is None else ctypes.byref(post_s),
-            None if next_s is None else ctypes.byref(next_s), x_out.data_ptr(), ldxo, op, ldo,
-            rows, C, max(1, rows // (groups or 1)), handle), "unstep_gate_residual_norm")
+    _call(lib().unstep_gate_residual_norm, "unstep_gate_residual_norm", index, stream,
+          (x.data_ptr(), xt, ldx, y.data_ptr(), ldy, gp, gt, gs, res_scale, pr, nr,
+           x_out.data_ptr(), ldxo, op, ldo, rows, C, (rows // groups if groups else rows) or 1))
     return x_out, out
 
 
