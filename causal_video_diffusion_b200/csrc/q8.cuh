@@ -42,8 +42,8 @@ __device__ __forceinline__ uint32_t q8_encode2(float lo, float hi, float inv, fl
 }
 
 // bf16 pairs that multiply raw codes (see q8_decode2) up to their values: 2^(E + 120) as the
-// product of two, because it exceeds bf16 for E > 7; the second, needed for bytes above
-// kQ8SplitByte alone, is NaN for a NaN block.
+// product of two, because it exceeds bf16 for E > 7; the second is 1 up to kQ8SplitByte, and NaN for
+// a NaN block.
 constexpr uint32_t kQ8SplitByte = 134;
 
 __device__ __forceinline__ uint32_t q8_mul1(uint32_t byte) {
@@ -51,7 +51,8 @@ __device__ __forceinline__ uint32_t q8_mul1(uint32_t byte) {
 }
 
 __device__ __forceinline__ uint32_t q8_mul2(uint32_t byte) {
-  return byte == kQ8NanByte ? 0x7FC07FC0u : (byte - kQ8SplitByte + 127u) * 0x00800080u;
+  return byte == kQ8NanByte ? 0x7FC07FC0u
+                            : (max(byte, kQ8SplitByte) - kQ8SplitByte + 127u) * 0x00800080u;
 }
 
 __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
@@ -60,17 +61,25 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
   return d;
 }
 
-// Two codes in bits 0-7 and 16-23 of w (other bits zero) -> a bf16 pair of their values times
-// 2^-120: sign to bit 15, the seven magnitude bits to bits 4-10 (e4m3's exponent bias is 7, bf16's
-// 127; subnormal codes become subnormal bf16 numbers of the same value).  16 w moves both by four
-// bits, 240 s the sign by the other four: multiply-adds, which the ALU pipe does not have to issue.
-__device__ __forceinline__ uint32_t q8_decode2(uint32_t w) {
-  return w * 16u + (w & 0x00800080u) * 240u;
+// q8_mul1 of a byte that stands in both halves of b2 and does not exceed kQ8SplitByte.
+__device__ __forceinline__ uint32_t q8_mul1_pair(uint32_t b2) { return b2 * 128u + 120u * 0x00800080u; }
+
+// Whether one of a word's four scale bytes exceeds kQ8SplitByte.
+__device__ __forceinline__ bool q8_any_split(uint32_t word) {
+  return __vmaxu4(word, kQ8SplitByte * 0x01010101u) != kQ8SplitByte * 0x01010101u;
 }
 
-// Four codes -> two bf16 pairs, times 2^-120.
+// Two sign-extended codes, one in each half of w -> a bf16 pair of their values times 2^-120: sign
+// in bit 15, the seven magnitude bits in bits 4-10 (e4m3's exponent bias is 7, bf16's 127; subnormal
+// codes become subnormal bf16 numbers of the same value).
+__device__ __forceinline__ uint32_t q8_decode2(uint32_t w) { return (w * 16u) & 0x87F087F0u; }
+
+// Four codes -> two bf16 pairs, times 2^-120.  A byte selector of 8 + i replicates byte i's sign.
 __device__ __forceinline__ uint2 q8_decode4(uint32_t c) {
-  return make_uint2(q8_decode2(__byte_perm(c, 0, 0x4140)), q8_decode2(__byte_perm(c, 0, 0x4342)));
+  uint32_t lo, hi;
+  asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(lo) : "r"(c));
+  asm("prmt.b32 %0, %1, 0, 0xB3A2;" : "=r"(hi) : "r"(c));
+  return make_uint2(q8_decode2(lo), q8_decode2(hi));
 }
 
 }  // namespace unstep

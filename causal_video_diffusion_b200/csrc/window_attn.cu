@@ -30,8 +30,8 @@
 // rescale; above it, the owning warp rescales its O rows in TMEM after the previous PV retired.
 //
 // Over an 8-bit cache (kQ8; 512 threads) K and V arrive as e4m3 codes under a power-of-two scale
-// per 32 channels, half the bytes, and every value is exactly a bf16 number.  Warps 12-15 copy a
-// key tile's codes into shared memory (cp.async, one tile ahead), decode them (about 2.5
+// per 32 channels, half the bytes, and every value is exactly a bf16 number.  Warp 10 copies a key
+// tile's codes into shared memory as they lie in the cache; warps 12-15 decode them (about 2.3
 // instructions an element), write the tile as bf16 into the stage that the TMA would have filled,
 // and announce it; rows behind the segment's end become zeros.  Everything behind the stage is the
 // bf16 kernel's.
@@ -467,106 +467,135 @@ UNSTEP_COLD_FN void merge_row(const AttnParams &p, int i, int row, long long t0,
   }
 }
 
-// A decoding thread's part of a half tile (the K or the V rows of a key tile): kSteps vectors of 16
-// codes, copied into slots of shared memory that only this thread uses (so its own wait for its
-// copies is all the synchronisation they need).  Step i is box (64 channels) i mod kBoxes of rows
-// 32 (i / kBoxes) ..; thread t takes its row t / 4 and channels 16 (t mod 4) ..: eight lanes store
-// to eight different chunks of the swizzled tile.  A warp's rows are 32 in all: lane l loads the
-// scales of its row l, and a step takes them by a shuffle.
-// The loop over the steps is rolled: a half tile decoded in straight-line code ran at 5.5 clocks
-// an instruction, its 17 KB and the softmax's putting each other out of the instruction cache.
+// A decoding thread's part of a half tile (the K or the V rows of a key tile, as loaded): four rows,
+// t / 4 + 32 g, and of each the 16 channels at 16 (t mod 4) of every 64-channel box.  Odd rows take
+// their two boxes in the other order, so that eight lanes read eight different 16-byte groups of the
+// codes (two rows) and store to eight different chunks of the swizzled tile.
+// Lane l holds the scale bytes of its warp's row l, 8 (l / 8) rows apart in groups; a vector takes
+// them by a shuffle.
+// The loop over the rows is rolled: a half tile decoded in straight-line code ran at 5.5 clocks an
+// instruction, its 17 KB and the softmax's putting each other out of the instruction cache.
 template <int D>
 struct Decoder {
-  static constexpr int kBoxes = D / 64, kSteps = 4 * kBoxes, kScales = D / kQ8Block;
-  int t, row, srow;   // row within a tile of step 0; row whose scales this lane loads
-  uint32_t slot;      // shared-memory address of this thread's vector 0 (K's; V's follow)
-  uint32_t d0, d1;    // where the two chunks of vector 0 go in stage 0's K tile
+  static constexpr int kBoxes = D / 64, kScales = D / kQ8Block;
+  int row, srow;         // first row; row whose scales this lane holds
+  uint32_t from;         // shared-memory address of vector 0's codes (K's; V's follow)
+  uint32_t d0, d1;       // where its two chunks go in stage 0's K tile, box 0
+  uint32_t odd;          // 1: boxes in the other order
+  uint32_t pick[kBoxes]; // byte selectors: a vector's scale byte into both halves of a word
+  int src_lane;          // lane that holds the first row's scales
 
-  __device__ __forceinline__ Decoder(int thread, const void *slots, const void *stages) {
-    t = thread;
+  __device__ __forceinline__ Decoder(int t, const void *codes, const void *stages) {
+    const int lane = t & 31;
     row = t >> 2;
-    srow = ((t & 31) >> 3) * 32 + (t >> 5) * 8 + (t & 7);
-    slot = smem_u32(slots) + t * 16;
+    srow = (lane >> 3) * 32 + (t >> 5) * 8 + (lane & 7);
+    odd = kBoxes == 2 ? row & 1 : 0;
+    from = smem_u32(codes) + row * D + (t & 3) * 16;
     const int c = (t & 3) * 2, x = row & 7;
     d0 = smem_u32(stages) + row * 128 + ((c ^ x) << 4);
     d1 = smem_u32(stages) + row * 128 + (((c + 1) ^ x) << 4);
+#pragma unroll
+    for (int k = 0; k < kBoxes; ++k) pick[k] = 0x4040u + (((k ^ odd) * 2) + (t >> 1 & 1)) * 0x0101u;
+    src_lane = lane >> 2;
   }
 
-  // Starts the copy of step i's vector; rows from `valid` on become zeros.  src: the tile's codes.
-  __device__ __forceinline__ void fetch(int i, uint32_t at, const unsigned char *src,
-                                        int valid) const {
-    const int r = i / kBoxes * 32 + row;
-    if (r < valid)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at),
-                   "l"(src + r * D + i % kBoxes * 64 + (t & 3) * 16)
-                   : "memory");
-    else
-      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
-  }
-
-  // Scale bytes of this lane's row.  src: the tile's scales.
+  // Scale bytes of this lane's row (1 behind `valid`).  src: the tile's scales.
   __device__ __forceinline__ uint32_t scales(const unsigned char *src, int valid) const {
     if (srow >= valid) return 0x7F7F7F7Fu;
     return D == 128 ? __ldg(reinterpret_cast<const uint32_t *>(src + srow * kScales))
                     : __ldg(reinterpret_cast<const uint16_t *>(src + srow * kScales));
   }
 
-  __device__ __forceinline__ void start(int half, const unsigned char *src, int valid) const {
+  // Decodes half tile `half` under the scales `word` into the swizzled bf16 tile `to` bytes behind
+  // stage 0's K tile.  kAny: scale bytes above kQ8SplitByte, rows from `valid` on (zeros) too.
+  template <bool kAny>
+  __device__ __forceinline__ void decode(int half, uint32_t word, uint32_t to, int valid) const {
+    uint32_t at = from + half * (128 * D);
 #pragma unroll 1
-    for (int i = 0; i < kSteps; ++i) fetch(i, slot + half * (128 * D) + i * 2048, src, valid);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  }
-
-  // Decodes half tile `half` under the scales `word` into the swizzled bf16 tile `tile` bytes
-  // behind stage 0's K tile, starting the copies of the next one (src, valid) as it goes.
-  __device__ __forceinline__ void decode(int half, uint32_t word, uint32_t tile,
-                                         const unsigned char *src, int valid) const {
-    constexpr int kU = 4;  // steps a turn: 2 measured 1-3 % slower
-    uint32_t at = slot + half * (128 * D), to = tile;
-#pragma unroll 1
-    for (int i0 = 0; i0 < kSteps; i0 += kU, at += 2048 * kU, to += 4096 * kU / kBoxes) {
-      uint32_t u[kU][4], byte[kU], o[kU][8], top = 0;
+    for (int g = 0; g < 4; ++g, at += 32 * D, to += 4096) {
+      uint32_t u[kBoxes][4], o[kBoxes][8];
 #pragma unroll
-      for (int k = 0; k < kU; ++k)
+      for (int k = 0; k < kBoxes; ++k)
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(u[k][0]), "=r"(u[k][1]), "=r"(u[k][2]), "=r"(u[k][3])
-                     : "r"(at + k * 2048));
+                     : "r"(at + (k ^ odd) * 64));
+      const uint32_t w = __shfl_sync(kFull, word, src_lane + g * 8);
 #pragma unroll
-      for (int k = 0; k < kU; ++k) {
-        const int i = i0 + k;
-        const uint32_t w = __shfl_sync(kFull, word, i / kBoxes * 8 + ((t & 31) >> 2));
-        byte[k] = (w >> ((t & 2) * 4 + i % kBoxes * 16)) & 0xFFu;
-        top = max(top, byte[k]);
-      }
-#pragma unroll
-      for (int k = 0; k < kU; ++k) {
-        const uint32_t m1 = q8_mul1(byte[k]);
+      for (int k = 0; k < kBoxes; ++k) {
+        const uint32_t byte2 = __byte_perm(w, 0, pick[k]);  // the scale byte, twice
+        const uint32_t m1 = kAny ? q8_mul1(byte2 & 0xFFu) : q8_mul1_pair(byte2);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint2 d = q8_decode4(u[k][e]);
           o[k][2 * e] = bf16x2_mul(d.x, m1);
           o[k][2 * e + 1] = bf16x2_mul(d.y, m1);
         }
+        if constexpr (kAny) {
+          const uint32_t m2 = q8_mul2(byte2 & 0xFFu);
+          const bool live = row + g * 32 < valid;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[k][e] = live ? bf16x2_mul(o[k][e], m2) : 0u;
+        }
       }
-      if (top > kQ8SplitByte) {
 #pragma unroll
-        for (int k = 0; k < kU; ++k)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[k][e] = bf16x2_mul(o[k][e], q8_mul2(byte[k]));
-      }
-#pragma unroll
-      for (int k = 0; k < kU; ++k) {
-        const uint32_t b = to + (k % kBoxes) * 16384 + k / kBoxes * 4096;
+      for (int k = 0; k < kBoxes; ++k) {
+        const uint32_t b = to + (k ^ odd) * 16384;
         asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(d0 + b), "r"(o[k][0]),
                      "r"(o[k][1]), "r"(o[k][2]), "r"(o[k][3])
                      : "memory");
         asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(d1 + b), "r"(o[k][4]),
                      "r"(o[k][5]), "r"(o[k][6]), "r"(o[k][7])
                      : "memory");
-        fetch(i0 + k, at + k * 2048, src, valid);
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+};
+
+// Copies `bytes` (a multiple of 16, both addresses on 16) into shared memory, completing on bar.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, int bytes, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Walks the key tiles of a CTA's segments in order, for the roles that need no more of them.
+struct TileWalk {
+  Seg sg;
+  int q, kt, row, valid;
+  long long head_row;  // first cache row of the segment's (stream, head)
+  bool more;
+
+  __device__ __forceinline__ void enter(const AttnParams &p, int cta, const SkRange &sk) {
+    more = get_seg(p, cta, sk, q, sg);
+    if (!more) {
+      valid = 0;
+      return;
+    }
+    head_row = static_cast<long long>(unit_pos(p, sg.u).bh) * p.rows;
+    kt = sg.k0;
+    key_tile(p, kt, row, valid);
+  }
+  __device__ __forceinline__ void start(const AttnParams &p, int cta, const SkRange &sk) {
+    q = 0;
+    row = 0;
+    head_row = 0;
+    enter(p, cta, sk);
+  }
+  __device__ __forceinline__ void next(const AttnParams &p, int cta, const SkRange &sk) {
+    if (++kt < sg.k1) {
+      key_tile(p, kt, row, valid);
+    } else {
+      ++q;
+      enter(p, cta, sk);
+    }
+  }
+  // Cache row (of all heads') of the tile's first key.
+  __device__ __forceinline__ long long first() const { return head_row + row; }
+  __device__ __forceinline__ bool sound(const AttnParams &p) const {
+    return row >= 0 && valid >= 1 && valid <= 128 && row + valid <= p.rows && head_row >= 0 &&
+           head_row < static_cast<long long>(p.B) * p.H * p.rows;
   }
 };
 
@@ -596,7 +625,9 @@ __global__ void __launch_bounds__((Cfg<D, kRopeQ, kQ8>::kThreads), 1)
   // free a period before V's, time that the decoding needs
   uint64_t *k_empty = q_rot + 1;
   uint64_t *v_full = k_empty + (kQ8 ? NS : 0);
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(v_full + (kQ8 ? NS : 0));
+  uint64_t *c_full = v_full + (kQ8 ? NS : 0);   // [2]: a tile's K codes, V codes have landed
+  uint64_t *c_empty = c_full + (kQ8 ? 2 : 0);   // [2]: and have been read, by four warps
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(c_empty + (kQ8 ? 2 : 0));
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   volatile int *merge_word = reinterpret_cast<volatile int *>(tmem_slot + 2);  // [2]
 
@@ -616,6 +647,10 @@ __global__ void __launch_bounds__((Cfg<D, kRopeQ, kQ8>::kThreads), 1)
       }
     }
     for (int i = 0; i < 2; ++i) {
+      if constexpr (kQ8) {
+        mbar_init(&c_full[i], 1);
+        mbar_init(&c_empty[i], 4);
+      }
       mbar_init(&s_full[i], 1);
       mbar_init(&p_ready[i], 128);
       mbar_init(&o_done[i], 1);
@@ -643,62 +678,39 @@ __global__ void __launch_bounds__((Cfg<D, kRopeQ, kQ8>::kThreads), 1)
       // ------------------------------------------------------------ K and V decoding
       const Decoder<D> dec(threadIdx.x & 127, smem + C::kSmemCodes, smem + C::kSmemKV);
       constexpr int kSc = Decoder<D>::kScales;
-      Seg sg{};
-      long long head_row = 0, row0 = 0;
-      int q = 0, kt = 0, valid = 0;
-      bool more = get_seg(p, cta, sk, 0, sg), ok = true;
-      auto locate = [&] {
-        int row;
-        key_tile(p, kt, row, valid);
-        row0 = head_row + row;
-        if (kDebugChecks && !debug_check(kt >= 0 && kt < p.n_tiles && row >= 0 && valid >= 1 &&
-                                             row + min(valid, 128) <= p.rows && row0 >= 0 &&
-                                             row0 < static_cast<long long>(p.B) * p.H * p.rows,
-                                         p.dev_error)) {
-          *abort_flag = 1;
-          valid = 0;
-        }
-      };
-      auto enter = [&] {
-        head_row = static_cast<long long>(unit_pos(p, sg.u).bh) * p.rows;
-        kt = sg.k0;
-        locate();
-      };
-      uint32_t word[2];
-      if (more) {
-        enter();
-        dec.start(0, p.q8.k_codes + row0 * D, valid);
-        dec.start(1, p.q8.v_codes + row0 * D, valid);
-        word[0] = dec.scales(p.q8.k_scale + row0 * kSc, valid);
-        word[1] = dec.scales(p.q8.v_scale + row0 * kSc, valid);
+      TileWalk tw;
+      tw.start(p, cta, sk);
+      uint32_t word[2] = {0, 0};
+      if (tw.more) {
+        word[0] = dec.scales(p.q8.k_scale + tw.first() * kSc, tw.valid);
+        word[1] = dec.scales(p.q8.v_scale + tw.first() * kSc, tw.valid);
       }
-      for (int n = 0; more && ok; ++n) {
-        const int s = n % NS;
+      bool ok = true;
+      for (int n = 0; ok && tw.more; ++n) {
+        const int s = n % NS, valid = tw.valid;
         const uint32_t par = (static_cast<uint32_t>(n / NS) & 1u) ^ 1u;
-        // the next tile's copies start as this one's slots are read
-        if (++kt < sg.k1) {
-          locate();
-        } else if ((more = get_seg(p, cta, sk, ++q, sg))) {
-          enter();
-        } else {
-          valid = 0;   // nothing follows
-        }
+        tw.next(p, cta, sk);
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
-          ok = __all_sync(kFull, wait_bounded(half ? &empty[s] : &k_empty[s], par, g, E));
+          ok = __all_sync(kFull, wait_bounded(half ? &empty[s] : &k_empty[s], par, g, E)) &&
+               __all_sync(kFull, wait_bounded(&c_full[half], static_cast<uint32_t>(n) & 1u, g, E));
           if (!ok) break;
+          // the next tile's scales, a tile ahead
           const uint32_t next =
-              dec.scales((half ? p.q8.v_scale : p.q8.k_scale) + row0 * kSc, valid);
-          asm volatile("cp.async.wait_group 1;" ::: "memory");  // the other half's may be open
-          dec.decode(half, word[0], static_cast<uint32_t>(s * C::kStageBytes + half * C::kTileBytes),
-                     (half ? p.q8.v_codes : p.q8.k_codes) + row0 * D, valid);
+              dec.scales((half ? p.q8.v_scale : p.q8.k_scale) + tw.first() * kSc, tw.valid);
+          const uint32_t to = static_cast<uint32_t>(s * C::kStageBytes + half * C::kTileBytes);
+          if (valid == 128 && !__any_sync(kFull, q8_any_split(word[0])))
+            dec.template decode<false>(half, word[0], to, valid);
+          else
+            dec.template decode<true>(half, word[0], to, valid);
           word[0] = word[1];
           word[1] = next;
           fence_proxy_async_smem();
           mbar_arrive(half ? &v_full[s] : &full[s]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c_empty[half]);
         }
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else if (warp >= 8) {
     regs_release<kQ8 ? kRegsIoQ8 : kRegsIo>();
@@ -763,6 +775,34 @@ __global__ void __launch_bounds__((Cfg<D, kRopeQ, kQ8>::kThreads), 1)
             wait_drain(&full[k % NS], static_cast<uint32_t>(k / NS) & 1u);
           if (nq > 0) wait_drain(q_full, static_cast<uint32_t>(nq - 1) & 1u);
         }
+      }
+      __syncwarp();
+    } else if (kQ8 && warp == 10) {
+      // -------------------------------------------------------------- 8-bit codes
+      if (lane == 0) {
+        TileWalk tw;
+        bool ok = true;
+        int n = 0;  // key tiles requested
+        int sent[2] = {0, 0};
+        for (tw.start(p, cta, sk); ok && tw.more; tw.next(p, cta, sk), ++n) {
+          if (kDebugChecks && !debug_check(tw.sound(p), p.dev_error)) {
+            *abort_flag = 1;
+            break;
+          }
+          for (int half = 0; half < 2; ++half) {
+            if (!(ok = wait_bounded(&c_empty[half], (static_cast<uint32_t>(n) & 1u) ^ 1u, g, E)))
+              break;
+            mbar_arrive_expect_tx(&c_full[half], tw.valid * D);
+            bulk_load(smem + C::kSmemCodes + half * 128 * D,
+                      (half ? p.q8.v_codes : p.q8.k_codes) + tw.first() * D, tw.valid * D,
+                      &c_full[half]);
+            sent[half] = n + 1;
+          }
+        }
+        // after an abort, every copy still in flight lands before the shared memory is released
+        if (*abort_flag)
+          for (int half = 0; half < 2; ++half)
+            if (sent[half] > 0) wait_drain(&c_full[half], static_cast<uint32_t>(sent[half] - 1) & 1u);
       }
       __syncwarp();
     } else if (warp == 9) {

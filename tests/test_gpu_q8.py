@@ -276,6 +276,25 @@ def test_attention_scale_range(cuda_lib, D, split):
     check_attn(shape, cache, q, 6)
 
 
+@pytest.mark.parametrize("D,split", [(64, (24, 20, 20)), (128, (44, 42, 42))])
+def test_attention_mixed_scales(cuda_lib, D, split):
+    """Blocks far apart in scale within a row, a tile and a thread's share of it: each 32 channels
+    of each value row have a magnitude of their own, on both sides of the split factor."""
+    shape = shape_of(1, 2, D, 10, 13, split)
+    cache = R.make_cache(shape, 3, 6)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    for c in range(4):
+        q, k, v = draw(shape, 30 + c, strong=False)
+        power = torch.randint(-30, 31, (1, shape.L, 2, D // 32, 1), generator=g, device="cuda")
+        v = torch.ldexp(v.float().unflatten(-1, (-1, 32)), power).flatten(-2).to(torch.bfloat16)
+        cache.rope_kv_append(q, k, v, c, 1)
+        for window in (1, 2, 3):
+            check_attn(shape, cache, q, window)
+    b = cache.v_scale.view(torch.uint8)
+    assert int(b.max()) > 134 > int(b.min())
+
+
 def test_attention_of_a_nan_key_is_nan(cuda_lib):
     shape = shape_of(1, 2, 64, 4, 6, (24, 20, 20))
     cache = R.make_cache(shape, 2, 4)
