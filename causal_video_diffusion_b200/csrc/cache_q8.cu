@@ -51,7 +51,9 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], uint32_t &byte) 
                     q8_encode2(x[4], x[5], inv, lim) | (q8_encode2(x[6], x[7], inv, lim) << 16));
 }
 
-template <int D>
+// kHeads heads a thread, H / kHeads apart, so that the item's coordinates and coefficients serve
+// all of them and 3 * kHeads loads are in flight.
+template <int D, int kHeads>
 __global__ void __launch_bounds__(kThreads) q8_rope_kv_append_kernel(const Q8AppendParams q,
                                                                       uint32_t n_items) {
   const RopeAppendParams &p = q.rope;
@@ -63,73 +65,93 @@ __global__ void __launch_bounds__(kThreads) q8_rope_kv_append_kernel(const Q8App
     }
   Item m;
   // n_items is a multiple of a block's four lanes, so a block's lanes are live together
-  const bool live = it < n_items && locate<D>(p, it, m);
-  uint4 qv = make_uint4(0, 0, 0, 0), kv = qv, vv = qv;
-  if (live) {
-    qv = ld_plain(static_cast<const __nv_bfloat16 *>(p.q) + m.e);
-    kv = ld_stream(static_cast<const __nv_bfloat16 *>(p.k) + m.e);
-    vv = ld_stream(static_cast<const __nv_bfloat16 *>(p.v) + m.e);
-  } else {
+  const bool live = it < n_items && locate<D>(p, it, m, kHeads);
+  if (!live) {
+    m.e = m.ce = 0;
 #pragma unroll
     for (int u = 0; u < 4; ++u) m.cs[u] = make_float2(0.f, 0.f);
   }
-  float kx[8], vx[8];
-  unpack8(kv, kx);
-  unpack8(vv, vx);
-  rotate8(kx, m.cs);
-  uint32_t kb, vb;
-  const uint2 kc = quantise8(kx, kb);
-  const uint2 vc = quantise8(vx, vb);
-  if (!live) return;
-  uint4 qo;
-  qo.x = rope_rotate_pair(qv.x, m.cs[0]);
-  qo.y = rope_rotate_pair(qv.y, m.cs[1]);
-  qo.z = rope_rotate_pair(qv.z, m.cs[2]);
-  qo.w = rope_rotate_pair(qv.w, m.cs[3]);
-  *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(q.q_out) + m.e) = qo;
-  *reinterpret_cast<uint2 *>(static_cast<unsigned char *>(p.k_cache) + m.ce) = kc;
-  *reinterpret_cast<uint2 *>(static_cast<unsigned char *>(p.v_cache) + m.ce) = vc;
-  if ((threadIdx.x & 3) == 0) {
-    q.k_scale[m.ce / kQ8Block] = static_cast<unsigned char>(kb);
-    q.v_scale[m.ce / kQ8Block] = static_cast<unsigned char>(vb);
+  const long long de = static_cast<long long>(p.H / kHeads) * D;
+  const long long dce = static_cast<long long>(p.H / kHeads) * p.rows * D;
+  uint4 qv[kHeads], kv[kHeads], vv[kHeads];
+#pragma unroll
+  for (int h = 0; h < kHeads; ++h) {
+    qv[h] = kv[h] = vv[h] = make_uint4(0, 0, 0, 0);
+    if (live) {
+      qv[h] = ld_plain(static_cast<const __nv_bfloat16 *>(p.q) + m.e + h * de);
+      kv[h] = ld_stream(static_cast<const __nv_bfloat16 *>(p.k) + m.e + h * de);
+      vv[h] = ld_stream(static_cast<const __nv_bfloat16 *>(p.v) + m.e + h * de);
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < kHeads; ++h) {
+    float kx[8], vx[8];
+    unpack8(kv[h], kx);
+    unpack8(vv[h], vx);
+    rotate8(kx, m.cs);
+    uint32_t kb, vb;
+    const uint2 kc = quantise8(kx, kb);
+    const uint2 vc = quantise8(vx, vb);
+    if (!live) continue;
+    uint4 qo;
+    qo.x = rope_rotate_pair(qv[h].x, m.cs[0]);
+    qo.y = rope_rotate_pair(qv[h].y, m.cs[1]);
+    qo.z = rope_rotate_pair(qv[h].z, m.cs[2]);
+    qo.w = rope_rotate_pair(qv[h].w, m.cs[3]);
+    const long long ce = m.ce + h * dce;
+    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(q.q_out) + m.e + h * de) = qo;
+    *reinterpret_cast<uint2 *>(static_cast<unsigned char *>(p.k_cache) + ce) = kc;
+    *reinterpret_cast<uint2 *>(static_cast<unsigned char *>(p.v_cache) + ce) = vc;
+    if ((threadIdx.x & 3) == 0) {
+      q.k_scale[ce / kQ8Block] = static_cast<unsigned char>(kb);
+      q.v_scale[ce / kQ8Block] = static_cast<unsigned char>(vb);
+    }
   }
 }
 
-// Sixteen codes (half a block) a thread: 16 bytes in, 32 out.
+// Eight codes of K and of V a thread and turn, two turns' loads at once: 8 bytes in, 16 out, so
+// that a warp's accesses are whole sectors on both sides.
 template <int D>
 __global__ void __launch_bounds__(kThreads) q8_cache_read_kernel(const Q8ReadParams p) {
-  constexpr int kVecs = D / 16;
+  constexpr int kVecs = D / 8, kTurns = 2;
   const long long n = static_cast<long long>(p.n_rows) * kVecs;
+  const long long step = static_cast<long long>(gridDim.x) * kThreads;
   for (long long head = blockIdx.y; head < p.heads; head += gridDim.y) {
-    for (long long it = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; it < n;
-         it += static_cast<long long>(gridDim.x) * kThreads) {
-      const int r = static_cast<int>(it / kVecs), c = static_cast<int>(it % kVecs);
-      const int row = r < p.seg_len[0] ? p.seg_row[0] + r : p.seg_row[1] + (r - p.seg_len[0]);
-      const long long src = (head * p.rows + row) * D + c * 16;
-      const long long dst = (head * p.n_rows + r) * D + c * 16;
+    for (long long i0 = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i0 < n;
+         i0 += step * kTurns) {
+      uint2 w[kTurns][2];
+      uint32_t byte[kTurns][2];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        void *out = t ? p.v_out : p.k_out;
-        if (!out) continue;
-        const uint4 w = *reinterpret_cast<const uint4 *>((t ? p.v_cache : p.k_cache) + src);
-        const uint32_t byte = (t ? p.v_scale : p.k_scale)[src / kQ8Block];
-        const uint32_t m1 = q8_mul1(byte);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-        uint32_t o[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint2 d = q8_decode4(u[i]);
-          o[2 * i] = bf16x2_mul(d.x, m1);
-          o[2 * i + 1] = bf16x2_mul(d.y, m1);
+      for (int k = 0; k < kTurns; ++k) {
+        const long long it = i0 + k * step;
+        if (it >= n) continue;
+        const int r = static_cast<int>(it / kVecs), c = static_cast<int>(it % kVecs);
+        const int row = r < p.seg_len[0] ? p.seg_row[0] + r : p.seg_row[1] + (r - p.seg_len[0]);
+        const long long src = (head * p.rows + row) * D + c * 8;
+        if (p.k_out) {
+          w[k][0] = *reinterpret_cast<const uint2 *>(p.k_cache + src);
+          byte[k][0] = p.k_scale[src / kQ8Block];
         }
-        if (byte > kQ8SplitByte) {
-          const uint32_t m2 = q8_mul2(byte);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = bf16x2_mul(o[i], m2);
+        if (p.v_out) {
+          w[k][1] = *reinterpret_cast<const uint2 *>(p.v_cache + src);
+          byte[k][1] = p.v_scale[src / kQ8Block];
         }
-        uint4 *d4 = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + dst);
-        d4[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        d4[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+#pragma unroll
+      for (int k = 0; k < kTurns; ++k) {
+        const long long it = i0 + k * step;
+        if (it >= n) continue;
+        const long long dst = head * p.n_rows * D + it * 8;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          void *out = t ? p.v_out : p.k_out;
+          if (!out) continue;
+          const uint32_t m1 = q8_mul1(byte[k][t]), m2 = q8_mul2(byte[k][t]);
+          const uint2 a = q8_decode4(w[k][t].x), b = q8_decode4(w[k][t].y);
+          *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + dst) =
+              make_uint4(bf16x2_mul(bf16x2_mul(a.x, m1), m2), bf16x2_mul(bf16x2_mul(a.y, m1), m2),
+                         bf16x2_mul(bf16x2_mul(b.x, m1), m2), bf16x2_mul(bf16x2_mul(b.y, m1), m2));
+        }
       }
     }
   }
@@ -140,27 +162,42 @@ __global__ void __launch_bounds__(kThreads) q8_cache_read_kernel(const Q8ReadPar
 cudaError_t launch_q8_rope_kv_append(const Q8AppendParams &in, cudaStream_t stream) {
   Q8AppendParams p = in;
   RopeAppendParams &r = p.rope;
-  const long long n_items = static_cast<long long>(r.B) * r.L * r.H * (r.D / 8);
+  if (r.D != 128 && r.D != 64) return cudaErrorInvalidValue;
+  const int heads = r.H % 4 == 0 ? 4 : r.H % 3 == 0 ? 3 : r.H % 2 == 0 ? 2 : 1;
+  const long long n_items = static_cast<long long>(r.B) * r.L * (r.H / heads) * (r.D / 8);
   if (n_items < 1 || n_items >= (1ll << 31) - kThreads) return cudaErrorInvalidConfiguration;
   r.slot0 = r.frame_idx % r.cap;
-  r.div_h = make_fastdiv(static_cast<uint32_t>(r.H));
+  r.div_h = make_fastdiv(static_cast<uint32_t>(r.H / heads));
+  if (heads > 1) r.sharded = 1;  // an item is not its offset / 8
   r.div_l = make_fastdiv(static_cast<uint32_t>(r.L));
   r.div_tf = make_fastdiv(static_cast<uint32_t>(r.Tf));
   r.div_wg = make_fastdiv(static_cast<uint32_t>(r.Wg));
   const unsigned blocks = static_cast<unsigned>((n_items + kThreads - 1) / kThreads);
   const uint32_t n = static_cast<uint32_t>(n_items);
-  if (r.D == 128)
-    q8_rope_kv_append_kernel<128><<<blocks, kThreads, 0, stream>>>(p, n);
-  else if (r.D == 64)
-    q8_rope_kv_append_kernel<64><<<blocks, kThreads, 0, stream>>>(p, n);
-  else
-    return cudaErrorInvalidValue;
+  const bool wide = r.D == 128;
+  switch (heads) {
+    case 4:
+      (wide ? q8_rope_kv_append_kernel<128, 4> : q8_rope_kv_append_kernel<64, 4>)
+          <<<blocks, kThreads, 0, stream>>>(p, n);
+      break;
+    case 3:
+      (wide ? q8_rope_kv_append_kernel<128, 3> : q8_rope_kv_append_kernel<64, 3>)
+          <<<blocks, kThreads, 0, stream>>>(p, n);
+      break;
+    case 2:
+      (wide ? q8_rope_kv_append_kernel<128, 2> : q8_rope_kv_append_kernel<64, 2>)
+          <<<blocks, kThreads, 0, stream>>>(p, n);
+      break;
+    default:
+      (wide ? q8_rope_kv_append_kernel<128, 1> : q8_rope_kv_append_kernel<64, 1>)
+          <<<blocks, kThreads, 0, stream>>>(p, n);
+  }
   return cudaGetLastError();
 }
 
 cudaError_t launch_q8_cache_read(const Q8ReadParams &p, cudaStream_t stream) {
-  const long long n = static_cast<long long>(p.n_rows) * (p.D / 16);
-  const long long bx = (n + kThreads - 1) / kThreads;
+  const long long n = static_cast<long long>(p.n_rows) * (p.D / 8);
+  const long long bx = (n + 2 * kThreads - 1) / (2 * kThreads);  // two turns a thread
   const dim3 grid(static_cast<unsigned>(bx < (1ll << 30) ? bx : (1ll << 30)),
                   static_cast<unsigned>(p.heads < 65535 ? p.heads : 65535));
   if (p.D == 128)

@@ -29,14 +29,16 @@ struct Item {
 // Where item `it` (one 8-channel vector of one (stream, token, head)) lives, and its coefficients.
 // All index arithmetic is 32-bit (items < 2^31, checked on the host) with multiply-high division.
 // Returns false only in the debug build, when an index falls outside its tensor (the item is
-// then skipped and the error word set).
+// then skipped and the error word set).  `heads`: items stand for that many heads each, H / heads
+// apart (div_h divides by H / heads), and are located at the first.
 template <int D>
-__device__ __forceinline__ bool locate(const RopeAppendParams &p, uint32_t it, Item &m) {
+__device__ __forceinline__ bool locate(const RopeAppendParams &p, uint32_t it, Item &m,
+                                       int heads = 1) {
   constexpr int kLogV = (D == 128) ? 4 : 3;  // 16-byte vectors per head row: D / 8
   const uint32_t c8 = it & ((1u << kLogV) - 1);
   const uint32_t r = it >> kLogV;             // (b*L + l)*H + h
   const uint32_t bl = fdiv(r, p.div_h);
-  const uint32_t h = r - bl * static_cast<uint32_t>(p.H);
+  const uint32_t h = r - bl * (static_cast<uint32_t>(p.H) / heads);
   const uint32_t b = fdiv(bl, p.div_l);
   const uint32_t l = bl - b * static_cast<uint32_t>(p.L);
   const uint32_t i = fdiv(l, p.div_tf);
