@@ -29,16 +29,15 @@ __device__ __forceinline__ uint32_t q8_scale_byte(uint32_t abs_bits) {
   return static_cast<uint32_t>(max(b, kQ8MinByte));
 }
 
-// 1 / 2^E of a scale byte (bytes 16 .. 247; 0 for a NaN block, whose codes are zeros).
+// 1 / 2^E of a scale byte (16 .. 247).
 __device__ __forceinline__ float q8_inv_scale(uint32_t byte) {
-  return byte == kQ8NanByte ? 0.f : __uint_as_float((254u - byte) << 23);
+  return __uint_as_float((254u - byte) << 23);
 }
 
-// Two values -> two codes (lo in the low byte).  lim is 448, or 240 under the top scale byte,
-// where 256 * 2^120 would already be infinite.
-__device__ __forceinline__ uint32_t q8_encode2(float lo, float hi, float inv, float lim) {
-  const float2 v = make_float2(fminf(fmaxf(lo * inv, -lim), lim), fminf(fmaxf(hi * inv, -lim), lim));
-  return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+// Two values -> two codes (lo in the low byte).  |x * inv| <= 448, but under the top scale byte up
+// to 512: there the caller clamps to 240 first, since 256 * 2^120 would already be infinite.
+__device__ __forceinline__ uint32_t q8_encode2(float lo, float hi, float inv) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo * inv, hi * inv), __NV_SATFINITE, __NV_E4M3);
 }
 
 // bf16 pairs that multiply raw codes (see q8_decode2) up to their values: 2^(E + 120) as the

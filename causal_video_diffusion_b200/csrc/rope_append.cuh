@@ -29,18 +29,26 @@ struct Item {
 // Where item `it` (one 8-channel vector of one (stream, token, head)) lives, and its coefficients.
 // All index arithmetic is 32-bit (items < 2^31, checked on the host) with multiply-high division.
 // Returns false only in the debug build, when an index falls outside its tensor (the item is
-// then skipped and the error word set).  `heads`: items stand for that many heads each, H / heads
-// apart (div_h divides by H / heads), and are located at the first.
-template <int D>
-__device__ __forceinline__ bool locate(const RopeAppendParams &p, uint32_t it, Item &m,
-                                       int heads = 1) {
+// then skipped and the error word set).
+// kHeads > 0: items stand for kHeads heads each, H / kHeads apart (div_h divides by H / kHeads), are
+// located at the first, and run through a head's tokens before the next head's.
+template <int D, int kHeads = 0>
+__device__ __forceinline__ bool locate(const RopeAppendParams &p, uint32_t it, Item &m) {
   constexpr int kLogV = (D == 128) ? 4 : 3;  // 16-byte vectors per head row: D / 8
   const uint32_t c8 = it & ((1u << kLogV) - 1);
-  const uint32_t r = it >> kLogV;             // (b*L + l)*H + h
-  const uint32_t bl = fdiv(r, p.div_h);
-  const uint32_t h = r - bl * (static_cast<uint32_t>(p.H) / heads);
-  const uint32_t b = fdiv(bl, p.div_l);
-  const uint32_t l = bl - b * static_cast<uint32_t>(p.L);
+  const uint32_t r = it >> kLogV;
+  uint32_t b, h, l;
+  if constexpr (kHeads == 0) {                // r = (b*L + l)*H + h
+    const uint32_t bl = fdiv(r, p.div_h);
+    h = r - bl * static_cast<uint32_t>(p.H);
+    b = fdiv(bl, p.div_l);
+    l = bl - b * static_cast<uint32_t>(p.L);
+  } else {                                    // r = (b*H/kHeads + h)*L + l
+    const uint32_t bh = fdiv(r, p.div_l);
+    l = r - bh * static_cast<uint32_t>(p.L);
+    b = fdiv(bh, p.div_h);
+    h = bh - b * (static_cast<uint32_t>(p.H) / kHeads);
+  }
   const uint32_t i = fdiv(l, p.div_tf);
   const uint32_t tok = l - i * static_cast<uint32_t>(p.Tf);
   const uint32_t y = fdiv(tok, p.div_wg);
@@ -49,9 +57,10 @@ __device__ __forceinline__ bool locate(const RopeAppendParams &p, uint32_t it, I
   int slot = p.slot0 + static_cast<int>(i);   // i < frames <= cap: one wrap at most
   if (slot >= p.cap) slot -= p.cap;
   // q, k, v: the shard's stream and head within the activations (it * 8 when unsharded)
-  m.e = p.sharded ? ((static_cast<long long>(p.b0) + b) * p.L + l) * p.act_H * D +
-                        (static_cast<long long>(p.h0) + h) * D + c8 * 8
-                  : static_cast<long long>(it) * 8;
+  m.e = kHeads > 0 || p.sharded
+            ? ((static_cast<long long>(p.b0) + b) * p.L + l) * p.act_H * D +
+                  (static_cast<long long>(p.h0) + h) * D + c8 * 8
+            : static_cast<long long>(it) * 8;
   m.ce = ((static_cast<long long>(b) * p.H + h) * p.rows + static_cast<long long>(slot) * p.Tf +
           tok) * D + c8 * 8;
   if (kDebugChecks) {
