@@ -7,6 +7,7 @@ library's kernels.  There is no fallback: if the library cannot be loaded, every
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import NamedTuple, Optional, Tuple
 
@@ -14,6 +15,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libunstep.so")
+HOST_PATH = os.path.join(_HERE, "_host_calls.so")
 
 UNSTEP_OK = 0
 UNSTEP_ERR_ARG = -1
@@ -425,41 +427,25 @@ class LayerCache:
         return out_h
 
 
-# The 8-bit cache's and the norms' calls take a few microseconds of host time, as long as their
-# kernels do for small chunks, so their checks use what torch answers fastest: the device's index
-# and the current stream's handle without the objects around them.
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+_HOST = None
 
 
-def _call(fn, name: str, index: int, stream: Optional[torch.cuda.Stream], args: tuple) -> None:
-    """``fn(*args, stream handle)`` with device `index` current; `stream` None: its current one."""
-    if stream is None:
-        handle = _current_stream(index)
-    elif stream.device_index != index:
-        raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on cuda:{index}")
-    else:
-        handle = stream.cuda_stream
-    if _current_device() == index:
-        rc = fn(*args, handle)
-    else:
-        with torch.cuda.device(index):
-            rc = fn(*args, handle)
-    if rc < 0:
-        raise UnstepError(rc, name)
-
-
-def _new_like(t: torch.Tensor, dtype: torch.dtype,
-              stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
-    """A contiguous output of t's shape that a call on `stream` writes: its memory is not reused
-    before the stream is done with it."""
-    if t.dtype is dtype:
-        out = torch.empty_like(t, memory_format=torch.contiguous_format)
-    else:
-        out = torch.empty(t.shape, dtype=dtype, device=t.device)
-    if stream is not None:
-        out.record_stream(stream)
-    return out
+def _host():
+    """The native side of the 8-bit cache's and the norms' calls (csrc/host_calls.cpp)."""
+    global _HOST
+    if _HOST is None:
+        L = lib()
+        if not os.path.exists(HOST_PATH):
+            raise RuntimeError(f"{HOST_PATH} is missing: the library has not been built "
+                               "(python -m causal_video_diffusion_b200.build)")
+        spec = importlib.util.spec_from_file_location("_host_calls", HOST_PATH)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.bind(UnstepError, *(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
+            "unstep_norm_modulate", "unstep_gate_residual_norm", "unstep_q8_rope_kv_append",
+            "unstep_q8_window_attn", "unstep_q8_cache_read")))
+        _HOST = m
+    return _HOST
 
 
 class LayerCacheQ8(LayerCache):
@@ -492,20 +478,11 @@ class LayerCacheQ8(LayerCache):
 
     def reset(self, stream: Optional[torch.cuda.Stream] = None) -> None:
         """Back to an empty cache, as after construction."""
-        self._ref = ctypes.byref(self.q8)
+        self._at = ctypes.addressof(self.q8)
         self._index = self.k_codes.get_device()
-        self._rows_like = {}     # frames -> a one-element tensor expanded to read_frames' shape
-        _call(lib().unstep_q8_cache_init, "unstep_q8_cache_init", self._index, stream,
-              (self._ref,))
-
-    def _act(self, t: torch.Tensor, frames: int, name: str) -> int:
-        """Address of a checked activation tensor of `frames` frames."""
-        c = self.c
-        if (t.dtype is torch.bfloat16 and t.get_device() == self._index and t.is_contiguous()
-                and t.shape == (self.act_B, frames * self.Tf, self.act_H, c.D)):
-            return t.data_ptr()
-        self._check_act(t, self.chunk_len(frames), name)
-        raise ValueError(f"{name} must be contiguous")
+        with torch.cuda.device(self.device):
+            _check(lib().unstep_q8_cache_init(ctypes.byref(self.q8), _stream_handle(stream)),
+                   "unstep_q8_cache_init")
 
     def rope_kv_append(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, frame_idx: int,
                        frames: int, stream: Optional[torch.cuda.Stream] = None,
@@ -515,17 +492,8 @@ class LayerCacheQ8(LayerCache):
         Returns the rotated q."""
         if defer_q:
             raise ValueError("an 8-bit cache rotates the queries in the append (no defer_q)")
-        qp = self._act(q, frames, "q")
-        kp, vp = self._act(k, frames, "k"), self._act(v, frames, "v")
-        op = qp
-        if q_out is None:
-            q_out = q
-        else:
-            op = self._act(q_out, frames, "q_out")
-        _call(lib().unstep_q8_rope_kv_append, "unstep_q8_rope_kv_append", self._index, stream,
-              (qp, op, kp, vp, self._ref, int(frame_idx),
-               unstep_grid_t(frames, self.c.Hg, self.c.Wg)))
-        return q_out
+        return (_HOST or _host()).q8_append(self._at, self._index, q, k, v, frame_idx, frames,
+                                            q_out, stream)
 
     def window_attn(self, q: torch.Tensor, window: int, out: Optional[torch.Tensor] = None,
                     stream: Optional[torch.cuda.Stream] = None,
@@ -533,13 +501,7 @@ class LayerCacheQ8(LayerCache):
         """Attention of the latest chunk's rotated queries over the last ``window`` frames."""
         if rope_q:
             raise ValueError("an 8-bit cache takes rotated queries (no rope_q)")
-        frames = self.c.last_chunk_frames
-        qp = self._act(q, frames, "q")
-        if out is None:
-            out = _new_like(q, torch.bfloat16, stream)
-        _call(lib().unstep_q8_window_attn, "unstep_q8_window_attn", self._index, stream,
-              (qp, self._ref, int(window), self._act(out, frames, "out")))
-        return out
+        return (_HOST or _host()).q8_attn(self._at, self._index, q, window, out, stream)
 
     def read_frames(self, first_frame: int, frames: int, k_out: Optional[torch.Tensor] = None,
                     v_out: Optional[torch.Tensor] = None,
@@ -547,29 +509,8 @@ class LayerCacheQ8(LayerCache):
                     ) -> Tuple[torch.Tensor, torch.Tensor]:
         """K (rotated) and V of frames ``first_frame .. first_frame+frames-1`` in time order, as
         bf16 ``[B][H][frames*Tf][D]``.  The ring must hold the frames."""
-        like = self._rows_like.get(frames)
-        if like is None:
-            c = self.c
-            if frames < 1 or frames > c.cap_frames:
-                raise UnstepError(UNSTEP_ERR_WINDOW if frames > 0 else UNSTEP_ERR_ARG, "read_frames")
-            like = torch.empty(1, dtype=torch.bfloat16, device=self.device)
-            like = like.expand(c.B, c.H, frames * self.Tf, c.D)
-            self._rows_like[frames] = like
-        k_out = self._rows_out(k_out, like, "k_out", stream)
-        v_out = self._rows_out(v_out, like, "v_out", stream)
-        _call(lib().unstep_q8_cache_read, "unstep_q8_cache_read", self._index, stream,
-              (self._ref, int(first_frame), frames, k_out.data_ptr(), v_out.data_ptr()))
-        return k_out, v_out
-
-    def _rows_out(self, t: Optional[torch.Tensor], like: torch.Tensor, name: str,
-                  stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
-        if t is None:
-            return _new_like(like, torch.bfloat16, stream)
-        if t.dtype is not torch.bfloat16 or t.shape != like.shape or \
-                t.get_device() != self._index or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous bfloat16 {tuple(like.shape)} on "
-                             f"{self.device}")
-        return t
+        return (_HOST or _host()).q8_read(self._at, self._index, first_frame, frames, k_out, v_out,
+                                          stream)
 
     def state_bytes(self) -> int:
         return lib().unstep_q8_cache_state_bytes(ctypes.byref(self.q8))
@@ -787,108 +728,6 @@ class Norm(NamedTuple):
     shift: Optional[torch.Tensor] = None
 
 
-_NORM_KINDS = {"layer": UNSTEP_NORM_LAYER, "rms": UNSTEP_NORM_RMS}
-_TYPES = {torch.bfloat16: UNSTEP_BF16, torch.float32: UNSTEP_F32}
-
-
-def _rows_of(t: torch.Tensor, name: str) -> Tuple[int, int]:
-    """(rows, row stride) of a tensor whose last axis is contiguous and whose leading axes walk
-    its rows at one stride."""
-    shape = t.shape
-    n = len(shape)
-    if n < 2:
-        raise ValueError(f"{name} must have a row axis and a channel axis")
-    C = shape[-1]
-    if n == 2:
-        rows = shape[0]
-        ld, st = t.stride()
-        if rows <= 1 or C == 0:
-            ld = C if rows <= 1 else ld
-            rows = rows if C else 0
-    else:
-        strides = t.stride()
-        st, rows, ld = strides[-1], 1, C
-        if t.numel() == 0:
-            return 0, C
-        for m, s in zip(reversed(shape[:-1]), reversed(strides[:-1])):
-            if m != 1:
-                if rows == 1:
-                    ld = s
-                elif s != ld * rows:
-                    raise ValueError(f"{name}'s rows must lie at one stride")
-                rows *= m
-    if C > 1 and st != 1:
-        raise ValueError(f"{name}'s channels must be contiguous")
-    if ld < C:
-        raise ValueError(f"{name}'s rows must not overlap")
-    return rows, ld
-
-
-def _vectors(t: torch.Tensor, C: int, groups: int, rows: int, name: str,
-             index: int) -> Tuple[int, int, int]:
-    """(pointer, group stride, groups) of a [G][C] modulation tensor; groups 0: not yet known."""
-    shape = t.shape
-    if len(shape) != 2 or shape[1] != C or t.get_device() != index or t.dtype not in _TYPES:
-        raise ValueError(f"{name} must be bf16 or fp32 [groups][{C}] on cuda:{index}")
-    G = shape[0]
-    ld, st = t.stride()
-    if st != 1:
-        raise ValueError(f"{name}'s channels must be contiguous")
-    if G < 1 or rows % G or (groups and groups != G):
-        raise ValueError(f"{name} has {G} groups for {rows} rows"
-                         + (f", other modulations {groups}" if groups else ""))
-    return t.data_ptr(), (ld if G > 1 else 0), G
-
-
-def _norm_struct(n: Norm, C: int, rows: int, groups: int, index: int):
-    """(unstep_norm_t, groups) of a Norm for `rows` rows of C channels."""
-    kind, eps, weight, bias, scale, shift = n
-    code = _NORM_KINDS.get(kind)
-    if code is None:
-        raise ValueError(f"norm kind {kind!r}: 'layer' or 'rms'")
-    dtype = wp = bp = cp = hp = None
-    ld = ld2 = 0
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is None:
-            continue
-        if t.shape != (C,) or t.get_device() != index or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous [{C}] on cuda:{index}")
-        if name == "weight":
-            wp, dtype = t.data_ptr(), t.dtype
-        else:
-            bp = t.data_ptr()
-            if dtype is None:
-                dtype = t.dtype
-    if scale is not None:
-        cp, ld, groups = _vectors(scale, C, groups, rows, "scale", index)
-        if dtype is None:
-            dtype = scale.dtype
-    if shift is not None:
-        hp, ld2, groups = _vectors(shift, C, groups, rows, "shift", index)
-        if dtype is None:
-            dtype = shift.dtype
-        if scale is not None and ld != ld2:
-            raise ValueError("scale and shift must have the same row stride")
-    ptype = UNSTEP_F32
-    if dtype is not None:
-        ptype = _TYPES.get(dtype, -1)
-        if ptype < 0 or (bias is not None and bias.dtype is not dtype) or \
-                (scale is not None and scale.dtype is not dtype) or \
-                (shift is not None and shift.dtype is not dtype):
-            raise ValueError("a norm's weight, bias, scale and shift must be all bf16 or all fp32")
-    return unstep_norm_t(code, eps, ptype, wp, bp, cp, hp, ld or ld2), groups
-
-
-def _norm_out(t: Optional[torch.Tensor], like: torch.Tensor, dtype: torch.dtype, name: str,
-              stream: Optional[torch.cuda.Stream]) -> Tuple[torch.Tensor, int]:
-    """(output, row stride): `t` checked against `like`, or a new contiguous tensor."""
-    if t is None:
-        return _new_like(like, dtype, stream), like.shape[-1]
-    if t.dtype is not dtype or t.shape != like.shape or t.get_device() != like.get_device():
-        raise ValueError(f"{name} must be {dtype} {tuple(like.shape)} on {like.device}")
-    return t, _rows_of(t, name)[1]
-
-
 def norm_modulate(x: torch.Tensor, norm: Norm, out: Optional[torch.Tensor] = None,
                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """``norm`` of every row of x (bf16 or fp32 ``[..., C]``, rows at one stride) as bf16.
@@ -896,17 +735,7 @@ def norm_modulate(x: torch.Tensor, norm: Norm, out: Optional[torch.Tensor] = Non
     The norm and modulation before a DiT block, or with a weight alone the norm of projected
     queries and keys.  ``out`` may be x itself when x is bf16.
     """
-    xt, index = _TYPES.get(x.dtype, -1), x.get_device()
-    if xt < 0 or index < 0:
-        raise ValueError("x must be a bf16 or fp32 CUDA tensor")
-    rows, ldx = _rows_of(x, "x")
-    C = x.shape[-1]
-    spec, groups = _norm_struct(norm, C, rows, 0, index)
-    out, ldo = _norm_out(out, x, torch.bfloat16, "out", stream)
-    _call(lib().unstep_norm_modulate, "unstep_norm_modulate", index, stream,
-          (x.data_ptr(), xt, ldx, out.data_ptr(), ldo, rows, C,
-           (rows // groups if groups else rows) or 1, ctypes.byref(spec)))
-    return out
+    return (_HOST or _host()).norm_modulate(x, norm, out, stream)
 
 
 def gate_residual_norm(x: torch.Tensor, y: torch.Tensor, gate: Optional[torch.Tensor] = None,
@@ -923,40 +752,8 @@ def gate_residual_norm(x: torch.Tensor, y: torch.Tensor, gate: Optional[torch.Te
     ``next`` None leaves the second output out (None).  ``next`` sees the fp32 sum, before it is
     rounded to x's type.  Returns (x_out, out).
     """
-    xt, index = _TYPES.get(x.dtype, -1), x.get_device()
-    if xt < 0 or index < 0:
-        raise ValueError("x must be a bf16 or fp32 CUDA tensor")
-    if y.dtype is not torch.bfloat16 or y.shape != x.shape or y.get_device() != index:
-        raise ValueError(f"y must be bfloat16 {tuple(x.shape)} on {x.device}")
-    rows, ldx = _rows_of(x, "x")
-    ldy = _rows_of(y, "y")[1]
-    C = x.shape[-1]
-    gp, gt, gs, groups = None, UNSTEP_F32, 0, 0
-    if gate is not None:
-        gp, gs, groups = _vectors(gate, C, 0, rows, "gate", index)
-        gt = _TYPES[gate.dtype]
-    pr = nr = op = None
-    ldo = 0
-    if post is not None:
-        spec, groups = _norm_struct(post, C, rows, groups, index)
-        pr = ctypes.byref(spec)
-    if next is not None:
-        spec, groups = _norm_struct(next, C, rows, groups, index)
-        nr = ctypes.byref(spec)
-    elif out is not None:
-        raise ValueError("out without a next norm")
-    ldxo = ldx
-    if x_out is None:
-        x_out = x
-    else:
-        x_out, ldxo = _norm_out(x_out, x, x.dtype, "x_out", stream)
-    if next is not None:
-        out, ldo = _norm_out(out, x, torch.bfloat16, "out", stream)
-        op = out.data_ptr()
-    _call(lib().unstep_gate_residual_norm, "unstep_gate_residual_norm", index, stream,
-          (x.data_ptr(), xt, ldx, y.data_ptr(), ldy, gp, gt, gs, res_scale, pr, nr,
-           x_out.data_ptr(), ldxo, op, ldo, rows, C, (rows // groups if groups else rows) or 1))
-    return x_out, out
+    return (_HOST or _host()).gate_residual_norm(x, y, gate, res_scale, post, next, x_out, out,
+                                                 stream)
 
 
 def selftest_wait_timeout(dev_error: torch.Tensor, limit_ns: int,
