@@ -4,15 +4,19 @@
 // A row lives in registers, spread over as many threads as hold one vector of 8 channels each (two
 // above 2048 channels, four above 8192): up to 256 channels part of a warp or a warp, behind that
 // whole warps.  Every statistic is taken from registers (the variance around the mean, in a second
-// pass) and each byte of x, y, x_out and h moves once.  The grid is persistent; a row's data are
-// loaded while the row before it is worked on.  Long chunks are bound by HBM and by issue slots (the
-// sums and addresses of so few channels a thread): the gated form moves 5.2 TB/s for 65536 rows of
-// 1536 channels, the norm alone 3.6 TB/s.  A whole row a warp costs fewer instructions, but its
-// serial chain of loads, sums and parameters is not hidden by the few warps that then fit: 4680
-// gated fp32 rows of 1536 take 47 us from a cold L2, 25 us this way.
+// pass) and each byte of x, y, x_out and h moves once.  The grid is persistent, a CTA takes
+// consecutive rows, and a row is loaded while the one before it is worked on; what all rows of a
+// group share (weight, bias, modulation, gate) is folded into one factor and one term a channel and
+// stays in registers until the group changes.  What bounds it is HBM for long chunks (30000 gated
+// fp32 rows of 1536 channels: 90 us, 6.1 TB/s; 65536 rows of the norm alone: 84 us, 4.8 TB/s), and
+// the chain of loads and two sums a row, which only many resident CTAs hide, for ordinary ones
+// (4680 rows of 1536: 18.7 us gated, 10.4 us the norm).  Measured instead for the gated 4680 rows:
+// parameters read for every row 22 us, two vectors a thread 22-24, a row a warp 29, two to four rows
+// loaded ahead 25-28 (fewer CTAs fit).  Above 8192 channels the parameters spill (2 TB/s).
 #include <cuda_bf16.h>
 
 #include "block_norm.h"
+#include "sm100.cuh"
 
 namespace unstep {
 namespace {
@@ -20,74 +24,92 @@ namespace {
 constexpr uint32_t kFullMask = 0xFFFFFFFFu;
 constexpr int kSms = 148;
 
-__device__ __forceinline__ void unpack8(const uint4 &w, float (&x)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-  }
+// Eight channels as four packed pairs (low, high) of fp32.
+struct Oct {
+  uint64_t p[4];
+};
+
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  uint32_t u[4];
+__device__ __forceinline__ uint64_t both(float x) { return f2_make(x, x); }
+
+__device__ __forceinline__ Oct zeros() { return Oct{{0, 0, 0, 0}}; }
+
+__device__ __forceinline__ Oct unpack8(const uint4 &w) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  Oct o;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+    o.p[i] = f2_make(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
+  return o;
+}
+
+__device__ __forceinline__ uint4 pack8(const Oct &o) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    f2_split(o.p[i], lo, hi);
+    u[i] = pack_bf16x2(lo, hi);
+  }
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
 // Eight fp32 values: one 32-byte access where the launch's fp32 pointers allow it (a lane's two
 // 16-byte ones use half of every sector they touch).
-__device__ __forceinline__ void load_f32(const float *s, bool wide, float (&x)[8]) {
+__device__ __forceinline__ Oct load_f32(const float *s, bool wide) {
+  Oct o;
   if (wide) {
-    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]),
-                   "=f"(x[6]), "=f"(x[7])
+    asm volatile("ld.global.v4.b64 {%0, %1, %2, %3}, [%4];"
+                 : "=l"(o.p[0]), "=l"(o.p[1]), "=l"(o.p[2]), "=l"(o.p[3])
                  : "l"(s)
                  : "memory");
   } else {
-    const float4 a = reinterpret_cast<const float4 *>(s)[0];
-    const float4 b = reinterpret_cast<const float4 *>(s)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    const ulonglong2 a = reinterpret_cast<const ulonglong2 *>(s)[0];
+    const ulonglong2 b = reinterpret_cast<const ulonglong2 *>(s)[1];
+    o = Oct{{a.x, a.y, b.x, b.y}};
   }
+  return o;
 }
 
-__device__ __forceinline__ void store_f32(float *d, bool wide, const float (&x)[8]) {
+__device__ __forceinline__ void store_f32(float *d, bool wide, const Oct &o) {
   if (wide) {
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "f"(x[0]),
-                 "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+    asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};" ::"l"(d), "l"(o.p[0]), "l"(o.p[1]),
+                 "l"(o.p[2]), "l"(o.p[3])
                  : "memory");
   } else {
-    reinterpret_cast<float4 *>(d)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4 *>(d)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    reinterpret_cast<ulonglong2 *>(d)[0] = make_ulonglong2(o.p[0], o.p[1]);
+    reinterpret_cast<ulonglong2 *>(d)[1] = make_ulonglong2(o.p[2], o.p[3]);
   }
 }
 
 // Eight parameters of either type (the same for the whole launch).
-__device__ __forceinline__ void param8(const void *p, int type, bool wide, long long at,
-                                       float (&x)[8]) {
-  if (type == UNSTEP_F32)
-    load_f32(static_cast<const float *>(p) + at, wide, x);
-  else
-    unpack8(*reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + at), x);
+__device__ __forceinline__ Oct param8(const void *p, int type, bool wide, long long at) {
+  if (type == UNSTEP_F32) return load_f32(static_cast<const float *>(p) + at, wide);
+  return unpack8(*reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + at));
 }
 
 // Vector v of this thread is channels 8 (first + v * kStep) .. of its row.
 template <int kLanes, int kVecs, int kWarps>
 struct Row {
   static constexpr int kStep = kLanes * kWarps;
-  using Values = float[kVecs][8];
+  static constexpr int kLine = (kWarps + 3) / 4 * 4;
   int first, vecs;           // vecs = C / 8
   float inv_c;
   bool wide;
-  float (*part)[kWarps];     // the warps' partial sums, one line for each sum of a row
+  float (*part)[kLine];      // the warps' partial sums, one line for each sum of a row
 
   __device__ __forceinline__ bool in(int v) const { return first + v * kStep < vecs; }
   __device__ __forceinline__ int channel(int v) const { return 8 * (first + v * kStep); }
 
-  __device__ __forceinline__ float sum(float s, int line) const {
+  __device__ __forceinline__ float sum(uint64_t s2, int line) const {
+    float lo, hi;
+    f2_split(s2, lo, hi);
+    float s = lo + hi;
 #pragma unroll
     for (int d = kLanes / 2; d > 0; d >>= 1) s += __shfl_xor_sync(kFullMask, s, d);
     if constexpr (kWarps > 1) {
@@ -95,62 +117,70 @@ struct Row {
       __syncthreads();
       s = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += part[line][w];
+      for (int w = 0; w < kLine; w += 4) {
+        const float4 q = *reinterpret_cast<const float4 *>(&part[line][w]);
+        s += q.x;
+        if (w + 1 < kWarps) s += q.y;
+        if (w + 2 < kWarps) s += q.z;
+        if (w + 3 < kWarps) s += q.w;
+      }
     }
     return s;
   }
 
-  // x -> norm(x), affine and modulated; lines `line` and `line + 1` of part.
-  __device__ __forceinline__ void norm(const unstep_norm_t &n, long long group, Values &x,
-                                       int line) const {
+  // x -> (x - mean) / sqrt(variance + eps) (RMS: mean 0) as x and the factor that is returned;
+  // lines `line` and `line + 1` of part.
+  __device__ __forceinline__ float normalise(const unstep_norm_t &n, Oct (&x)[kVecs],
+                                             int line) const {
     if (n.kind == UNSTEP_NORM_LAYER) {
-      float s = 0.f;
+      uint64_t s = 0;
 #pragma unroll
       for (int v = 0; v < kVecs; ++v)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += x[v][i];  // zeros behind the row's end
-      const float mean = sum(s, line) * inv_c;
+        for (int i = 0; i < 4; ++i) s = fadd2(s, x[v].p[i]);  // zeros behind the row's end
+      const uint64_t shift = both(-sum(s, line) * inv_c);
 #pragma unroll
       for (int v = 0; v < kVecs; ++v)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[v][i] -= mean;
+        for (int i = 0; i < 4; ++i) x[v].p[i] = fadd2(x[v].p[i], shift);
     }
-    float s = 0.f;
+    uint64_t s = 0;
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
-      float q = 0.f;
+      uint64_t q = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q = fmaf(x[v][i], x[v][i], q);
-      if (in(v)) s += q;
+      for (int i = 0; i < 4; ++i) q = ffma2(x[v].p[i], x[v].p[i], q);
+      if (in(v)) s = fadd2(s, q);
     }
-    const float rstd = rsqrtf(fmaf(sum(s, line + 1), inv_c, n.eps));
+    return rsqrtf(fmaf(sum(s, line + 1), inv_c, n.eps));
+  }
+
+  // A norm's affine part and modulation for a group, as one factor and one term a channel:
+  // (n * weight + bias) * (1 + scale) + shift = n * a + c.
+  __device__ __forceinline__ void parameters(const unstep_norm_t &n, long long group,
+                                             Oct (&a)[kVecs], Oct (&c)[kVecs]) const {
     const long long mod = group * n.mod_stride;
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
+      const int ch = channel(v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[v].p[i] = both(1.f);
+      c[v] = zeros();
       if (!in(v)) continue;
-      const int c = channel(v);
-      float q[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[v][i] *= rstd;
-      if (n.weight) {
-        param8(n.weight, n.param_type, wide, c, q);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[v][i] *= q[i];
-      }
-      if (n.bias) {
-        param8(n.bias, n.param_type, wide, c, q);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[v][i] += q[i];
-      }
+      if (n.weight) a[v] = param8(n.weight, n.param_type, wide, ch);
+      if (n.bias) c[v] = param8(n.bias, n.param_type, wide, ch);
       if (n.scale) {
-        param8(n.scale, n.param_type, wide, mod + c, q);
+        const Oct q = param8(n.scale, n.param_type, wide, mod + ch);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[v][i] = fmaf(x[v][i], q[i], x[v][i]);
+        for (int i = 0; i < 4; ++i) {
+          a[v].p[i] = ffma2(a[v].p[i], q.p[i], a[v].p[i]);
+          c[v].p[i] = ffma2(c[v].p[i], q.p[i], c[v].p[i]);
+        }
       }
       if (n.shift) {
-        param8(n.shift, n.param_type, wide, mod + c, q);
+        const Oct q = param8(n.shift, n.param_type, wide, mod + ch);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[v][i] += q[i];
+        for (int i = 0; i < 4; ++i) c[v].p[i] = fadd2(c[v].p[i], q.p[i]);
       }
     }
   }
@@ -161,117 +191,172 @@ constexpr int threads_of() {
   return kWarps > 1 ? 32 * kWarps : 128;
 }
 
-// CTAs of an SM: registers for the row, the next row and y beside it.
-template <int kVecs, int kWarps, bool kF32, bool kGated>
+enum Mode { kNorm, kGated, kGatedPost };  // h = next(x); with the residual sum; and post(y) in it
+
+// CTAs of an SM: registers for the row, the next row, y beside them, and the parameters.
+template <int kVecs, int kWarps, bool kF32, Mode kMode>
 constexpr int ctas_of() {
-  constexpr int regs = 44 + kVecs * (8 + (kF32 ? 8 : 4) + (kGated ? 12 : 0));
+  constexpr int regs = 24 + kVecs * ((kF32 ? 16 : 12) + 16 + (kMode == kNorm ? 0 : 20) +
+                                     (kMode == kGatedPost ? 8 : 0));
   constexpr int n = 65536 / threads_of<kWarps>() / ((regs + 7) / 8 * 8);
   return n < 1 ? 1 : (n > 2048 / threads_of<kWarps>() ? 2048 / threads_of<kWarps>() : n);
 }
 
-template <int kLanes, int kVecs, int kWarps, bool kF32, bool kGated>
-__global__ void __launch_bounds__(threads_of<kWarps>(), (ctas_of<kVecs, kWarps, kF32, kGated>()))
+template <int kLanes, int kVecs, int kWarps, bool kF32, Mode kMode>
+__global__ void __launch_bounds__(threads_of<kWarps>(), (ctas_of<kVecs, kWarps, kF32, kMode>()))
     block_norm_kernel(const NormParams p) {
   constexpr int kRows = threads_of<kWarps>() / (kLanes * kWarps);  // rows of a CTA at once
-  __shared__ float part[kWarps > 1 ? 8 : 1][kWarps];
-  Row<kLanes, kVecs, kWarps> row;
+  using Place = Row<kLanes, kVecs, kWarps>;
+  __shared__ __align__(16) float part[kWarps > 1 ? 8 : 1][Place::kLine];
+  Place row;
   row.first = threadIdx.x % (kLanes * kWarps);
   row.vecs = p.C / 8;
   row.inv_c = 1.f / static_cast<float>(p.C);
   row.wide = p.wide;
-  const long long step = static_cast<long long>(gridDim.x) * kRows;
-  long long r = static_cast<long long>(blockIdx.x) * kRows + threadIdx.x / (kLanes * kWarps);
-  float xn[kVecs][kF32 ? 8 : 1];       // the next row, as loaded
+  // this CTA's turns: consecutive sets of kRows rows, so that the group seldom changes
+  const long long b = blockIdx.x;
+  const long long set0 = b * p.sets + (b < p.extra ? b : p.extra);
+  const long long set1 = set0 + p.sets + (b < p.extra ? 1 : 0);
+  long long r = set0 * kRows + threadIdx.x / (kLanes * kWarps);
+  // this thread's vector 0 in row r of each tensor
+  constexpr int kX = kF32 ? 4 : 2;
+  const char *px = static_cast<const char *>(p.x) + (r * p.ldx + row.channel(0)) * kX;
+  const char *py = nullptr;
+  char *po = nullptr;
+  if constexpr (kMode != kNorm) {
+    py = static_cast<const char *>(p.y) + (r * p.ldy + row.channel(0)) * 2;
+    po = static_cast<char *>(p.x_out) + (r * p.ldxo + row.channel(0)) * kX;
+  }
+  char *ph = static_cast<char *>(p.h) + (r * p.ldh + row.channel(0)) * 2;
+  // the next row as loaded; behind a row's end and behind the last row whatever was there before,
+  // zeros to begin with (no sum of a row that is stored takes it in)
+  Oct xn[kF32 ? kVecs : 1];
   uint4 xw[kVecs], yw[kVecs];
-  auto fetch = [&](long long at) {
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v) {
+    if constexpr (kF32) xn[v] = zeros();
+    xw[v] = yw[v] = make_uint4(0, 0, 0, 0);
+  }
+  auto fetch = [&] {
+    constexpr int kStride = 8 * Place::kStep;
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
-      if (at >= p.rows || !row.in(v)) continue;
-      const int c = row.channel(v);
+      if (!row.in(v)) continue;
       if constexpr (kF32)
-        load_f32(static_cast<const float *>(p.x) + at * p.ldx + c, p.wide, xn[v]);
+        xn[v] = load_f32(reinterpret_cast<const float *>(px) + v * kStride, p.wide);
       else
-        xw[v] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.x) +
-                                                 at * p.ldx + c);
-      if constexpr (kGated)
-        yw[v] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.y) +
-                                                 at * p.ldy + c);
+        xw[v] = *reinterpret_cast<const uint4 *>(px + v * kStride * 2);
+      if constexpr (kMode != kNorm) yw[v] = *reinterpret_cast<const uint4 *>(py + v * kStride * 2);
     }
   };
-  fetch(r);
-  // a CTA's threads take the same number of turns: rows behind the last are zeros, unstored
-  long long base = static_cast<long long>(blockIdx.x) * kRows;
-  for (int turn = 0; base < p.rows; base += step, r += step, turn ^= 4) {
+  if (r < p.rows) fetch();
+  // the group's parameters: h = n(x) * a + c, x_out = x + n(y) * ga + gc
+  Oct a[kVecs], c[kVecs], ga[kVecs], gc[kVecs];
+  long long group = -1;
+  for (long long set = set0; set < set1; ++set) {
     // the sums' lines alternate: a warp may still read this turn's when another starts the next
-    row.part = part + (kWarps > 1 ? turn : 0);
+    if constexpr (kWarps > 1) row.part = part + (set & 1) * 4;
     const bool live = r < p.rows;
-    const long long g = p.narrow ? static_cast<long long>(fdiv(static_cast<uint32_t>(r), p.div_group))
-                                 : r / p.rows_per_group;
-    float x[kVecs][8];
-    float y[kGated ? kVecs : 1][8];
+    const long long g =
+        !live ? 0 : p.narrow ? static_cast<long long>(fdiv(static_cast<uint32_t>(r), p.div_group))
+                             : r / p.rows_per_group;
+    if (g != group) {
+      group = g;
+      if (p.h) row.parameters(p.next, g, a, c);
+      if constexpr (kMode != kNorm) {
+        if constexpr (kMode == kGatedPost) row.parameters(p.post, g, ga, gc);
+        const uint64_t res = both(p.res_scale);
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) {
+          Oct q;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) q.p[i] = res;
+          if (p.gate && row.in(v)) {
+            q = param8(p.gate, p.gate_type, p.wide, g * p.gate_stride + row.channel(v));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q.p[i] = fmul2(q.p[i], res);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            ga[v].p[i] = kMode == kGatedPost ? fmul2(ga[v].p[i], q.p[i]) : q.p[i];
+            if constexpr (kMode == kGatedPost) gc[v].p[i] = fmul2(gc[v].p[i], q.p[i]);
+          }
+        }
+      }
+    }
+    Oct x[kVecs], y[kVecs];
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
-      const bool on = live && row.in(v);
-      if constexpr (kF32) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[v][i] = on ? xn[v][i] : 0.f;
-      } else {
-        unpack8(on ? xw[v] : make_uint4(0, 0, 0, 0), x[v]);
-      }
-      if constexpr (kGated) unpack8(on ? yw[v] : make_uint4(0, 0, 0, 0), y[v]);
+      if constexpr (kF32)
+        x[v] = xn[v];
+      else
+        x[v] = unpack8(xw[v]);
+      if constexpr (kMode != kNorm) y[v] = unpack8(yw[v]);
     }
-    fetch(r + step);
-    if constexpr (kGated) {
-      if (p.has_post) row.norm(p.post, live ? g : 0, y, 0);
+    r += kRows;
+    px += kRows * p.ldx * kX;
+    if constexpr (kMode != kNorm) py += kRows * p.ldy * 2;
+    if (r < p.rows && set + 1 < set1) fetch();
+    if constexpr (kMode != kNorm) {
+      uint64_t rstd = both(1.f);
+      if constexpr (kMode == kGatedPost) rstd = both(row.normalise(p.post, y, 0));
 #pragma unroll
       for (int v = 0; v < kVecs; ++v) {
-        if (!live || !row.in(v)) continue;
-        const int c = row.channel(v);
-        if (p.gate) {
-          float q[8];
-          param8(p.gate, p.gate_type, p.wide, g * p.gate_stride + c, q);
+        if (!row.in(v)) continue;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[v][i] *= q[i];
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (kMode == kGatedPost) {
+            x[v].p[i] = fadd2(x[v].p[i], ffma2(y[v].p[i], fmul2(rstd, ga[v].p[i]), gc[v].p[i]));
+          } else {
+            x[v].p[i] = ffma2(y[v].p[i], ga[v].p[i], x[v].p[i]);
+          }
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[v][i] = fmaf(p.res_scale, y[v][i], x[v][i]);
+        if (!live) continue;
         if constexpr (kF32)
-          store_f32(static_cast<float *>(p.x_out) + r * p.ldxo + c, p.wide, x[v]);
+          store_f32(reinterpret_cast<float *>(po) + v * 8 * Place::kStep, p.wide, x[v]);
         else
-          *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.x_out) + r * p.ldxo + c) =
-              pack8(x[v]);
+          *reinterpret_cast<uint4 *>(po + v * 16 * Place::kStep) = pack8(x[v]);
       }
+      po += kRows * p.ldxo * kX;
       if (!p.h) continue;
     }
-    row.norm(p.next, live ? g : 0, x, kGated ? 2 : 0);
+    const uint64_t rstd = both(row.normalise(p.next, x, kMode == kNorm ? 0 : 2));
 #pragma unroll
-    for (int v = 0; v < kVecs; ++v)
-      if (live && row.in(v))
-        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.h) + r * p.ldh +
-                                   row.channel(v)) = pack8(x[v]);
+    for (int v = 0; v < kVecs; ++v) {
+      if (!live || !row.in(v)) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[v].p[i] = ffma2(x[v].p[i], fmul2(rstd, a[v].p[i]), c[v].p[i]);
+      *reinterpret_cast<uint4 *>(ph + v * 16 * Place::kStep) = pack8(x[v]);
+    }
+    ph += kRows * p.ldh * 2;
   }
 }
 
-template <int kLanes, int kVecs, int kWarps, bool kF32, bool kGated>
-void start(const NormParams &p, cudaStream_t stream) {
+template <int kLanes, int kVecs, int kWarps, bool kF32, Mode kMode>
+void start(const NormParams &in, cudaStream_t stream) {
   constexpr int kThreads = threads_of<kWarps>(), kRows = kThreads / (kLanes * kWarps);
-  constexpr long long kMost = static_cast<long long>(kSms) * ctas_of<kVecs, kWarps, kF32, kGated>();
-  const long long blocks = (p.rows + kRows - 1) / kRows;
-  block_norm_kernel<kLanes, kVecs, kWarps, kF32, kGated>
-      <<<static_cast<unsigned>(blocks < kMost ? blocks : kMost), kThreads, 0, stream>>>(p);
+  constexpr long long kMost = static_cast<long long>(kSms) * ctas_of<kVecs, kWarps, kF32, kMode>();
+  NormParams p = in;
+  const long long sets = (p.rows + kRows - 1) / kRows, grid = sets < kMost ? sets : kMost;
+  p.sets = sets / grid;
+  p.extra = sets % grid;
+  block_norm_kernel<kLanes, kVecs, kWarps, kF32, kMode>
+      <<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(p);
 }
 
 template <int kLanes, int kVecs, int kWarps>
 cudaError_t launch(const NormParams &p, bool gated, cudaStream_t stream) {
   const bool f32 = p.x_type == UNSTEP_F32;
-  if (gated && f32)
-    start<kLanes, kVecs, kWarps, true, true>(p, stream);
-  else if (gated)
-    start<kLanes, kVecs, kWarps, false, true>(p, stream);
-  else if (f32)
-    start<kLanes, kVecs, kWarps, true, false>(p, stream);
+  if (!gated)
+    f32 ? start<kLanes, kVecs, kWarps, true, kNorm>(p, stream)
+        : start<kLanes, kVecs, kWarps, false, kNorm>(p, stream);
+  else if (!p.has_post)
+    f32 ? start<kLanes, kVecs, kWarps, true, kGated>(p, stream)
+        : start<kLanes, kVecs, kWarps, false, kGated>(p, stream);
   else
-    start<kLanes, kVecs, kWarps, false, false>(p, stream);
+    f32 ? start<kLanes, kVecs, kWarps, true, kGatedPost>(p, stream)
+        : start<kLanes, kVecs, kWarps, false, kGatedPost>(p, stream);
   return cudaGetLastError();
 }
 

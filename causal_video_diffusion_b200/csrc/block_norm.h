@@ -25,6 +25,7 @@ struct NormParams {
   // pointer on 32 bytes (row and group strides are multiples of 8 elements)
   bool narrow, wide;
   FastDiv div_group;
+  long long sets, extra;  // sets of rows a CTA takes; the first `extra` CTAs take one more
 };
 
 // gated = false: h = next(x).  gated = true: x_out = x + res_scale * gate * post(y), h = next of it.
