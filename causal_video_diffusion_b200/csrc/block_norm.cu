@@ -218,6 +218,8 @@ __global__ void __launch_bounds__(threads_of<kWarps>(), (ctas_of<kVecs, kWarps, 
   const long long set0 = b * p.sets + (b < p.extra ? b : p.extra);
   const long long set1 = set0 + p.sets + (b < p.extra ? 1 : 0);
   long long r = set0 * kRows + threadIdx.x / (kLanes * kWarps);
+  let_successor_start();
+  wait_for_predecessor();
   // this thread's vector 0 in row r of each tensor
   constexpr int kX = kF32 ? 4 : 2;
   const char *px = static_cast<const char *>(p.x) + (r * p.ldx + row.channel(0)) * kX;
@@ -334,30 +336,28 @@ __global__ void __launch_bounds__(threads_of<kWarps>(), (ctas_of<kVecs, kWarps, 
 }
 
 template <int kLanes, int kVecs, int kWarps, bool kF32, Mode kMode>
-void start(const NormParams &in, cudaStream_t stream) {
+cudaError_t start(const NormParams &in, cudaStream_t stream) {
   constexpr int kThreads = threads_of<kWarps>(), kRows = kThreads / (kLanes * kWarps);
   constexpr long long kMost = static_cast<long long>(kSms) * ctas_of<kVecs, kWarps, kF32, kMode>();
   NormParams p = in;
   const long long sets = (p.rows + kRows - 1) / kRows, grid = sets < kMost ? sets : kMost;
   p.sets = sets / grid;
   p.extra = sets % grid;
-  block_norm_kernel<kLanes, kVecs, kWarps, kF32, kMode>
-      <<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(p);
+  return launch_overlapped(block_norm_kernel<kLanes, kVecs, kWarps, kF32, kMode>,
+                           dim3(static_cast<unsigned>(grid)), kThreads, 0, stream, p);
 }
 
 template <int kLanes, int kVecs, int kWarps>
 cudaError_t launch(const NormParams &p, bool gated, cudaStream_t stream) {
   const bool f32 = p.x_type == UNSTEP_F32;
   if (!gated)
-    f32 ? start<kLanes, kVecs, kWarps, true, kNorm>(p, stream)
-        : start<kLanes, kVecs, kWarps, false, kNorm>(p, stream);
-  else if (!p.has_post)
-    f32 ? start<kLanes, kVecs, kWarps, true, kGated>(p, stream)
-        : start<kLanes, kVecs, kWarps, false, kGated>(p, stream);
-  else
-    f32 ? start<kLanes, kVecs, kWarps, true, kGatedPost>(p, stream)
-        : start<kLanes, kVecs, kWarps, false, kGatedPost>(p, stream);
-  return cudaGetLastError();
+    return f32 ? start<kLanes, kVecs, kWarps, true, kNorm>(p, stream)
+               : start<kLanes, kVecs, kWarps, false, kNorm>(p, stream);
+  if (!p.has_post)
+    return f32 ? start<kLanes, kVecs, kWarps, true, kGated>(p, stream)
+               : start<kLanes, kVecs, kWarps, false, kGated>(p, stream);
+  return f32 ? start<kLanes, kVecs, kWarps, true, kGatedPost>(p, stream)
+             : start<kLanes, kVecs, kWarps, false, kGatedPost>(p, stream);
 }
 
 }  // namespace

@@ -65,6 +65,8 @@ template <int D, int kHeads>
 __global__ void __launch_bounds__(kAppendThreads, 6) q8_rope_kv_append_kernel(const Q8AppendParams q,
                                                                       uint32_t n_items) {
   const RopeAppendParams &p = q.rope;
+  let_successor_start();
+  wait_for_predecessor();
   const uint32_t it = blockIdx.x * kAppendThreads + threadIdx.x;
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < p.frames; i += kAppendThreads) {
@@ -124,6 +126,8 @@ __global__ void __launch_bounds__(kThreads) q8_cache_read_kernel(const Q8ReadPar
   constexpr int kVecs = D / 8, kTurns = 2;
   const long long n = static_cast<long long>(p.n_rows) * kVecs;
   const long long step = static_cast<long long>(gridDim.x) * kThreads;
+  let_successor_start();
+  wait_for_predecessor();
   for (long long head = blockIdx.y; head < p.heads; head += gridDim.y) {
     for (long long i0 = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i0 < n;
          i0 += step * kTurns) {
@@ -182,24 +186,19 @@ cudaError_t launch_q8_rope_kv_append(const Q8AppendParams &in, cudaStream_t stre
   const unsigned blocks = static_cast<unsigned>((n_items + kAppendThreads - 1) / kAppendThreads);
   const uint32_t n = static_cast<uint32_t>(n_items);
   const bool wide = r.D == 128;
+  auto run = [&](auto kernel) {
+    return launch_overlapped(kernel, dim3(blocks), kAppendThreads, 0, stream, p, n);
+  };
   switch (heads) {
     case 4:
-      (wide ? q8_rope_kv_append_kernel<128, 4> : q8_rope_kv_append_kernel<64, 4>)
-          <<<blocks, kAppendThreads, 0, stream>>>(p, n);
-      break;
+      return run(wide ? q8_rope_kv_append_kernel<128, 4> : q8_rope_kv_append_kernel<64, 4>);
     case 3:
-      (wide ? q8_rope_kv_append_kernel<128, 3> : q8_rope_kv_append_kernel<64, 3>)
-          <<<blocks, kAppendThreads, 0, stream>>>(p, n);
-      break;
+      return run(wide ? q8_rope_kv_append_kernel<128, 3> : q8_rope_kv_append_kernel<64, 3>);
     case 2:
-      (wide ? q8_rope_kv_append_kernel<128, 2> : q8_rope_kv_append_kernel<64, 2>)
-          <<<blocks, kAppendThreads, 0, stream>>>(p, n);
-      break;
+      return run(wide ? q8_rope_kv_append_kernel<128, 2> : q8_rope_kv_append_kernel<64, 2>);
     default:
-      (wide ? q8_rope_kv_append_kernel<128, 1> : q8_rope_kv_append_kernel<64, 1>)
-          <<<blocks, kAppendThreads, 0, stream>>>(p, n);
+      return run(wide ? q8_rope_kv_append_kernel<128, 1> : q8_rope_kv_append_kernel<64, 1>);
   }
-  return cudaGetLastError();
 }
 
 cudaError_t launch_q8_cache_read(const Q8ReadParams &p, cudaStream_t stream) {
@@ -207,13 +206,9 @@ cudaError_t launch_q8_cache_read(const Q8ReadParams &p, cudaStream_t stream) {
   const long long bx = (n + 2 * kThreads - 1) / (2 * kThreads);  // two turns a thread
   const dim3 grid(static_cast<unsigned>(bx < (1ll << 30) ? bx : (1ll << 30)),
                   static_cast<unsigned>(p.heads < 65535 ? p.heads : 65535));
-  if (p.D == 128)
-    q8_cache_read_kernel<128><<<grid, kThreads, 0, stream>>>(p);
-  else if (p.D == 64)
-    q8_cache_read_kernel<64><<<grid, kThreads, 0, stream>>>(p);
-  else
-    return cudaErrorInvalidValue;
-  return cudaGetLastError();
+  if (p.D != 128 && p.D != 64) return cudaErrorInvalidValue;
+  return launch_overlapped(p.D == 128 ? q8_cache_read_kernel<128> : q8_cache_read_kernel<64>, grid,
+                           kThreads, 0, stream, p);
 }
 
 }  // namespace unstep

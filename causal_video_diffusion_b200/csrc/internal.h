@@ -25,6 +25,36 @@ inline FastDiv make_fastdiv(uint32_t d) {
 }
 
 #ifdef __CUDACC__
+// Launch overlap.  A kernel launched by launch_overlapped may start while its predecessor on the
+// stream still runs: its blocks set themselves up, and every thread calls wait_for_predecessor()
+// before it touches global memory (it returns when the predecessor has completed and its writes are
+// visible).  let_successor_start() allows the next such launch the same.  Chains of short calls gain
+// the launch and set-up of each: 72 x 128 norms back to back 4.2 -> 2.7 us, attention of 72 queries
+// 10.3 -> 7.6 us.
+__device__ __forceinline__ void let_successor_start() {
+  asm volatile("griddepcontrol.launch_dependents;");
+}
+__device__ __forceinline__ void wait_for_predecessor() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <class... Params, class... Args>
+cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
+                              cudaStream_t stream, const Args &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 // Index checks of the debug build (compiled with -DUNSTEP_DEBUG; empty otherwise): a failed
 // check records UNSTEP_ERR_DEVICE_BOUNDS (-10) in the caller's error word, and the caller skips
 // the access or winds the CTA down through its abort path.  Nothing ever traps.

@@ -668,6 +668,12 @@ __global__ void __launch_bounds__((Cfg<D, kRopeQ, kQ8>::kThreads), 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if constexpr (kQ8) {
+    // not before this CTA holds its TMEM: a successor that took it first and then waited for this
+    // grid would wait for good
+    let_successor_start();
+    wait_for_predecessor();
+  }
   const WaitGuard g{abort_flag, p.dev_error, p.wait_limit_ns};
   constexpr int E = UNSTEP_ERR_DEVICE_TIMEOUT;
   const SkRange sk = sk_range(p, cta);
@@ -1138,6 +1144,9 @@ cudaError_t launch_d(const CUtensorMap &tq, const CUtensorMap &tk, const CUtenso
     if (dev < 64) __atomic_fetch_or(&attr_set, bit, __ATOMIC_RELEASE);
   }
   if (p.grid < 1) return cudaErrorInvalidConfiguration;
+  if constexpr (kQ8)
+    return launch_overlapped(window_attn_kernel<D, kRopeQ, kQ8>, dim3(static_cast<unsigned>(p.grid)),
+                             C::kThreads, C::kSmemAlloc, stream, tq, tk, tv, p);
   window_attn_kernel<D, kRopeQ, kQ8>
       <<<static_cast<unsigned>(p.grid), C::kThreads, C::kSmemAlloc, stream>>>(tq, tk, tv, p);
   return cudaGetLastError();
