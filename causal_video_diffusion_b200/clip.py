@@ -24,22 +24,23 @@ LATENT_CHANNELS = 16
 
 class ClipDriver:
     def __init__(self, workload: W.Workload, layers: Optional[int] = None, kind: str = "unstep",
-                 seed: int = 0, device: Optional[torch.device] = None):
+                 seed: int = 0, device: Optional[torch.device] = None, cache: str = "bf16"):
+        """``cache``: "bf16", or "q8" for layers that keep K and V in 8 bits (LayerCacheQ8)."""
+        if cache not in ("bf16", "q8"):
+            raise ValueError(f"cache {cache!r}: 'bf16' or 'q8'")
+        make = binding.LayerCacheQ8 if cache == "q8" else binding.LayerCache
         self.wl = workload
         self.shape = s = workload.shape
         self.layers = workload.layers if layers is None else layers
         self.sched = S.clip_schedule(kind, workload.chunks)
         self.device = dev = torch.device(device) if device is not None else torch.device(
             "cuda", torch.cuda.current_device())
-        first = binding.LayerCache(s.B, s.H, s.D, s.Hg, s.Wg, s.d_t, s.d_h, s.d_w,
-                                   cap_frames=workload.cap,
-                                   max_pos_t=workload.frame_idx(workload.chunks), device=dev)
+        first = make(s.B, s.H, s.D, s.Hg, s.Wg, s.d_t, s.d_h, s.d_w, cap_frames=workload.cap,
+                     max_pos_t=workload.frame_idx(workload.chunks), device=dev)
         # one attention scratch for every layer: their calls are ordered on one stream
         self.caches = [first] + [
-            binding.LayerCache(s.B, s.H, s.D, s.Hg, s.Wg, s.d_t, s.d_h, s.d_w,
-                               cap_frames=workload.cap,
-                               max_pos_t=workload.frame_idx(workload.chunks), device=dev,
-                               scratch=first.scratch)
+            make(s.B, s.H, s.D, s.Hg, s.Wg, s.d_t, s.d_h, s.d_w, cap_frames=workload.cap,
+                 max_pos_t=workload.frame_idx(workload.chunks), device=dev, scratch=first.scratch)
             for _ in range(self.layers - 1)]
         self.inputs = []   # [forward][layer] -> (q, k, v)
         for n, f in enumerate(self.sched):

@@ -826,6 +826,12 @@ int check_ready_q8(const unstep_q8_cache_t *c) {
   return UNSTEP_OK;
 }
 
+// Whether two ranges of `bytes` bytes share one.
+bool overlap(const void *a, const void *b, size_t bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y ? y - x < bytes : x - y < bytes;
+}
+
 // Ring rows of `count` frames from frame f0 on: at most two ranges.
 void ring_rows(const unstep_cache_t *c, int f0, int count, int (&row)[2], int (&len)[2]) {
   const int tf = c->Hg * c->Wg, s0 = f0 % c->cap_frames;
@@ -881,6 +887,12 @@ int unstep_q8_rope_kv_append(const void *q, void *q_out, const void *k, const vo
   const long long rows = static_cast<long long>(grid.frames) * c->Hg * c->Wg;
   if (rows > INT_MAX || static_cast<long long>(c->B) * c->H > (1ll << 31) / (c->D / 8) / rows - 1)
     return UNSTEP_ERR_UNSUPPORTED;
+  // q_out == q rotates in place; k and v are read while q_out is written
+  const size_t chunk = 2ull * static_cast<size_t>(act_B(c)) * static_cast<size_t>(rows) *
+                       static_cast<size_t>(act_H(c)) * static_cast<size_t>(c->D);
+  if (overlap(q_out, k, chunk) || overlap(q_out, v, chunk) ||
+      (q_out != q && overlap(q_out, q, chunk)))
+    return UNSTEP_ERR_ARG;
   unstep::Q8AppendParams p{};
   p.rope = append_params(c, k, v, frame_idx, grid);
   p.rope.q = const_cast<void *>(q);  // read only

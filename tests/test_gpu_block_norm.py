@@ -156,6 +156,33 @@ def test_strided_rows_and_surroundings(cuda_lib):
     assert bool((x[:, C:] == 9).all()) and bool((h[:, C:] == 5).all())
 
 
+@pytest.mark.parametrize("C", [72, 1536, 2056])
+def test_fp32_off_32_bytes(cuda_lib, C):
+    """fp32 rows and parameters on 16-byte but not 32-byte addresses: the same bits as on 32."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(C)
+
+    def off(t, by=4):
+        flat = torch.full((t.numel() + 16,), 7.0, dtype=t.dtype, device="cuda")
+        view = flat[by: by + t.numel()].view(t.shape)
+        view.copy_(t)
+        return view, flat
+
+    x, y, w = rand(g, 6, C), rand(g, 6, C).to(BF), rand(g, C)
+    tab = rand(g, 3, C)
+    n = Norm("layer", 1e-6, w, w, tab, tab)
+    m = Norm("layer", 1e-6, off(w)[0], off(w, 12)[0], off(tab)[0], off(tab, 12)[0])
+    want = binding.norm_modulate(x, n)
+    assert torch.equal(binding.norm_modulate(off(x)[0], m), want)
+    assert torch.equal(binding.norm_modulate(x, m), want)
+    assert torch.equal(binding.norm_modulate(off(x, 12)[0], n), want)
+    want = binding.gate_residual_norm(x, y, gate=tab, post=n, next=n, x_out=torch.empty_like(x))
+    xo, flat = off(torch.zeros_like(x), 12)
+    got = binding.gate_residual_norm(off(x)[0], y, gate=off(tab)[0], post=m, next=m, x_out=xo)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert bool((flat[:12] == 7).all()) and bool((flat[12 + xo.numel():] == 7).all())
+
+
 def test_difficult_rows(cuda_lib):
     """Constant rows, zeros, one large channel, a large common offset, NaN and infinity in one row
     of several that share a CTA; eps 0 on a row with variance."""
@@ -273,6 +300,14 @@ def test_binding_refusals(cuda_lib):
         lambda: binding.gate_residual_norm(x, x.clone(), gate=w2, next=Norm(scale=torch.zeros((3, 64), device="cuda"))),
         lambda: binding.gate_residual_norm(x, x.clone(), out=x.clone()),
         lambda: binding.gate_residual_norm(x, x.clone(), x_out=x.float()),
+        lambda: binding.gate_residual_norm(x, x.clone(), x_out=x.cpu()),
+        lambda: binding.gate_residual_norm(x, x.clone(), res_scale="1"),
+        lambda: binding.norm_modulate(x, ("layer", 1e-6)),
+        lambda: binding.norm_modulate(x, Norm(3)),
+        lambda: binding.norm_modulate(x, Norm(weight=1.0)),
+        lambda: binding.norm_modulate(x, Norm(eps=None)),
+        lambda: binding.norm_modulate([1.0], Norm()),
+        lambda: binding.norm_modulate(torch.zeros((), dtype=BF, device="cuda"), Norm()),
     ]
     for i, f in enumerate(bad):
         with pytest.raises(ValueError):

@@ -400,6 +400,16 @@ def test_bf16_calls_refuse_the_8bit_cache(cuda_lib):
         c.window_attn(q, 1, rope_q=True)
     with pytest.raises(ValueError):
         c.rope_kv_append(q.float(), k, v, 1, 1)
+    for args in ((q.cpu(), k, v, 1, 1), (q, k[:, :1], v, 1, 1), (q, k, v, 1, 2), (q, k, v, 1, -1),
+                 (q, k, v, 2 ** 40, 1), (q, k, v, 1.5, 1), (q, k, None, 1, 1),
+                 (q.transpose(1, 2).contiguous().transpose(1, 2), k, v, 1, 1)):
+        with pytest.raises(ValueError):
+            c.rope_kv_append(*args)
+    with pytest.raises(binding.UnstepError):
+        c.rope_kv_append(q, k, v, 1, 1, q_out=k)
+    with pytest.raises(ValueError):
+        c.window_attn(q, 1, out=q[:, :, :1])
+    assert c.frames_written == 1 and c.last_chunk == (0, 1)
     with pytest.raises(ValueError):
         c.read_frames(0, 1, k_out=torch.empty(1, device="cuda", dtype=torch.bfloat16))
 

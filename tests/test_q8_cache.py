@@ -91,6 +91,17 @@ def test_append_refusals(L):
     q.k_scale = None
     assert append(c=q) == B.UNSTEP_ERR_ARG
     assert (q.base.frames_written, q.base.last_chunk_start) == (9, 6)
+    # q_out over k, v or part of q: the last thing checked before a launch
+    n = 2 * c_elements(cache(), 3)
+    far = P + 4 * n
+    for kw in (dict(qo=P, k=P, v=far), dict(qo=P, k=far, v=P), dict(qo=far, k=far + n - 16, v=P),
+               dict(qo=far, k=P, v=far - n + 16), dict(q=far + 16, qo=far, k=P, v=P)):
+        assert append(**kw) == B.UNSTEP_ERR_ARG, kw
+
+
+def c_elements(q, frames):
+    c = q.base
+    return c.B * frames * c.Hg * c.Wg * c.H * c.D
 
 
 def test_attention_and_read_refusals(L):
