@@ -887,12 +887,12 @@ int unstep_q8_rope_kv_append(const void *q, void *q_out, const void *k, const vo
   const long long rows = static_cast<long long>(grid.frames) * c->Hg * c->Wg;
   if (rows > INT_MAX || static_cast<long long>(c->B) * c->H > (1ll << 31) / (c->D / 8) / rows - 1)
     return UNSTEP_ERR_UNSUPPORTED;
-  // q_out == q rotates in place; k and v are read while q_out is written
+  // a thread reads its elements of q, k and v before it writes those of q_out: q_out may be one of
+  // them, but not lie across one
   const size_t chunk = 2ull * static_cast<size_t>(act_B(c)) * static_cast<size_t>(rows) *
                        static_cast<size_t>(act_H(c)) * static_cast<size_t>(c->D);
-  if (overlap(q_out, k, chunk) || overlap(q_out, v, chunk) ||
-      (q_out != q && overlap(q_out, q, chunk)))
-    return UNSTEP_ERR_ARG;
+  for (const void *in : {q, k, v})
+    if (in != q_out && overlap(q_out, in, chunk)) return UNSTEP_ERR_ARG;
   unstep::Q8AppendParams p{};
   p.rope = append_params(c, k, v, frame_idx, grid);
   p.rope.q = const_cast<void *>(q);  // read only

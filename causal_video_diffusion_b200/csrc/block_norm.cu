@@ -29,12 +29,6 @@ struct Oct {
   uint64_t p[4];
 };
 
-__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 __device__ __forceinline__ uint64_t both(float x) { return f2_make(x, x); }
 
 __device__ __forceinline__ Oct zeros() { return Oct{{0, 0, 0, 0}}; }

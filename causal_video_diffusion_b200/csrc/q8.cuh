@@ -14,6 +14,8 @@
 
 #include <cstdint>
 
+#include "sm100.cuh"
+
 namespace unstep {
 
 constexpr int kQ8Block = 32;             // channels that share a scale
@@ -37,7 +39,10 @@ __device__ __forceinline__ float q8_inv_scale(uint32_t byte) {
 // Two values -> two codes (lo in the low byte).  |x * inv| <= 448, but under the top scale byte up
 // to 512: there the caller clamps to 240 first, since 256 * 2^120 would already be infinite.
 __device__ __forceinline__ uint32_t q8_encode2(float lo, float hi, float inv) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(lo * inv, hi * inv), __NV_SATFINITE, __NV_E4M3);
+  const uint64_t inv2 = f2_make(inv, inv);
+  float a, b;
+  f2_split(fmul2(f2_make(lo, hi), inv2), a, b);
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
 // bf16 pairs that multiply raw codes (see q8_decode2) up to their values: 2^(E + 120) as the

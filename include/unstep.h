@@ -414,7 +414,7 @@ int unstep_q8_cache_init(unstep_q8_cache_t *cache, unstep_stream_t stream);
 /*
  * unstep_rope_kv_append into an 8-bit cache: k is rotated and v copied, both are quantised as
  * they are written.  The rotated queries go to q_out, bf16 in q's layout; q_out == q rotates in
- * place, any other overlap of q_out with q, k or v is refused (ARG).  For a shard cache only the shard's streams and heads
+ * place.  q_out may be q, k or v itself, but not overlap one of them otherwise (ARG).  For a shard cache only the shard's streams and heads
  * of q_out are written.  Frame order, slots and metadata as in unstep_rope_kv_append.
  * Errors: those of unstep_rope_kv_append, plus UNSUPPORTED for 2^31 or more 8-channel vectors in
  * the chunk.

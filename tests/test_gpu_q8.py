@@ -87,6 +87,11 @@ def test_append_matches_the_definition(cuda_lib, dims):
             assert torch.equal(was[:, :, keep], t.view(torch.uint8)[:, :, keep])
         assert torch.equal(cache.slot_frame, bf.slot_frame)
         assert cache.last_chunk == bf.last_chunk and cache.frames_written == bf.frames_written
+    # onto k itself, re-forwarding the same chunk: k is read before its place is written
+    codes = cache.k_codes.view(torch.uint8).clone()
+    over = k.clone()
+    assert cache.rope_kv_append(q, over, v, 3 * F, F, q_out=over) is over
+    assert torch.equal(over, q_out) and torch.equal(cache.k_codes.view(torch.uint8), codes)
     # in place, re-forwarding the same chunk: the same rows
     codes = cache.k_codes.view(torch.uint8).clone()
     assert cache.rope_kv_append(q, k, v, 3 * F, F) is q
@@ -405,8 +410,10 @@ def test_bf16_calls_refuse_the_8bit_cache(cuda_lib):
                  (q.transpose(1, 2).contiguous().transpose(1, 2), k, v, 1, 1)):
         with pytest.raises(ValueError):
             c.rope_kv_append(*args)
+    both = torch.empty(2 * q.numel(), dtype=q.dtype, device="cuda")
+    a, b = both[: q.numel()].view_as(q), both[64: 64 + q.numel()].view_as(q)
     with pytest.raises(binding.UnstepError):
-        c.rope_kv_append(q, k, v, 1, 1, q_out=k)
+        c.rope_kv_append(q, a, v, 1, 1, q_out=b)
     with pytest.raises(ValueError):
         c.window_attn(q, 1, out=q[:, :, :1])
     assert c.frames_written == 1 and c.last_chunk == (0, 1)

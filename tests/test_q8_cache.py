@@ -91,11 +91,11 @@ def test_append_refusals(L):
     q.k_scale = None
     assert append(c=q) == B.UNSTEP_ERR_ARG
     assert (q.base.frames_written, q.base.last_chunk_start) == (9, 6)
-    # q_out over k, v or part of q: the last thing checked before a launch
+    # q_out across q, k or v: the last thing checked before a launch
     n = 2 * c_elements(cache(), 3)
     far = P + 4 * n
-    for kw in (dict(qo=P, k=P, v=far), dict(qo=P, k=far, v=P), dict(qo=far, k=far + n - 16, v=P),
-               dict(qo=far, k=P, v=far - n + 16), dict(q=far + 16, qo=far, k=P, v=P)):
+    for kw in (dict(qo=P + 16), dict(qo=far, k=far + n - 16), dict(qo=far, v=far - n + 16),
+               dict(q=far + 16, qo=far)):
         assert append(**kw) == B.UNSTEP_ERR_ARG, kw
 
 
