@@ -74,8 +74,8 @@ def load_peaks():
         return dict(FALLBACK_PEAKS), "fallback"
 
 
-ATTN_SOURCES = ("window_attn.cu", "sm100.cuh", "internal.h", "limits.h")
-ROPE_SOURCES = ("rope_append.cu", "internal.h", "limits.h")
+ATTN_SOURCES = ("window_attn.cu", "q8.cuh", "sm100.cuh", "internal.h", "limits.h")
+ROPE_SOURCES = ("rope_append.cu", "rope_append.cuh", "internal.h", "limits.h")
 GEMM_SOURCES = ("gemm2sm.cu", "sm100.cuh", "gemm.h", "limits.h")
 CONV_SOURCES = ("conv3d.cu", "sm100.cuh", "conv3d.h", "limits.h")
 

@@ -16,6 +16,7 @@
 #include <cuda_bf16.h>
 
 #include "block_norm.h"
+#include "internal.h"
 #include "sm100.cuh"
 
 namespace unstep {

@@ -180,7 +180,7 @@ Rows rows_of(const at::Tensor &t, const char *name) {
 struct Batch {
   int index;
   long long rows, C, groups;  // groups 0: no modulation seen yet
-  long long per_group() const { return groups ? rows / groups : (rows ? rows : 1); }
+  long long per_group() const { return rows ? rows / (groups ? groups : 1) : 1; }
 };
 
 struct Vectors {

@@ -75,6 +75,13 @@ __device__ __forceinline__ uint32_t fdiv(uint32_t x, const FastDiv &f) {
   return (__umulhi(x, f.m) + x) >> f.l;
 }
 
+// Product of packed fp32 pairs (see sm100.cuh's fadd2 and ffma2).
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // One RoPE channel pair, two packed bf16 (a = low half, b = high half), rotated by (c, s):
 // (a c - b s, a s + b c) in fp32, each rounded to bf16 (RNE).  The append kernel and the
 // attention's query prologue both rotate through this function, so both give the same bits.

@@ -14,6 +14,7 @@
 
 #include <cstdint>
 
+#include "internal.h"
 #include "sm100.cuh"
 
 namespace unstep {

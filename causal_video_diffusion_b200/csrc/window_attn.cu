@@ -660,6 +660,9 @@ __global__ void __launch_bounds__((Cfg<D, kRopeQ, kQ8>::kThreads), 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
+  // TMEM is taken after the predecessor has ended and before a successor may start: a CTA that held
+  // it while it waited for a grid with a CTA on this SM that still needs it would wait for good
+  if constexpr (kQ8) wait_for_predecessor();
   if (warp == 8) {
     tmem_alloc(tmem_slot, C::kTmCols);
     tmem_relinquish();
@@ -668,12 +671,7 @@ __global__ void __launch_bounds__((Cfg<D, kRopeQ, kQ8>::kThreads), 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if constexpr (kQ8) {
-    // not before this CTA holds its TMEM: a successor that took it first and then waited for this
-    // grid would wait for good
-    let_successor_start();
-    wait_for_predecessor();
-  }
+  if constexpr (kQ8) let_successor_start();
   const WaitGuard g{abort_flag, p.dev_error, p.wait_limit_ns};
   constexpr int E = UNSTEP_ERR_DEVICE_TIMEOUT;
   const SkRange sk = sk_range(p, cta);

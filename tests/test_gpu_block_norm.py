@@ -214,6 +214,8 @@ def test_rows_of_none_and_of_many_groups(cuda_lib):
     assert binding.norm_modulate(z, Norm()).shape == (0, 64)
     x_out, h = binding.gate_residual_norm(z, z, next=Norm())
     assert x_out is z and h.shape == (0, 64)
+    m = torch.zeros((3, 64), device="cuda")
+    assert binding.norm_modulate(z, Norm(scale=m, shift=m)).shape == (0, 64)
     g = torch.Generator(device="cuda")
     g.manual_seed(8)
     # a modulation for every row, and one shared by expanding it

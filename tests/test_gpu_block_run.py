@@ -111,6 +111,30 @@ def test_calls_in_a_row_need_no_waits(cuda_lib):
     assert all(torch.equal(a, b) for a, b in zip(*results))
 
 
+def test_norms_around_the_projections(cuda_lib):
+    """Norms before and after the library's own products, which also start while their predecessor
+    ends: many in a row give the bits of the same calls with a wait after each."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(12)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(BF)  # noqa: E731
+    w1, w2 = r(192, 256) / 16, r(256, 192) / 14
+    x0, n = r(300, 256), Norm("layer", 1e-6, weight=1 + r(256) / 8)
+    results = []
+    for wait in (torch.cuda.synchronize, lambda: None):
+        x, got = x0.clone(), []
+        for _ in range(40):
+            h = binding.norm_modulate(x, n)
+            wait()
+            y = binding.lowrank_linear(h, w1, w2)
+            wait()
+            x, h = binding.gate_residual_norm(x, y, res_scale=0.5, next=n, x_out=torch.empty_like(x))
+            wait()
+            got += [x, h]
+        torch.cuda.synchronize()
+        results.append(got)
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
 def test_block_in_a_graph(cuda_lib):
     """Three layers captured once and replayed on new inputs, against eager calls on a second set."""
     shape = shape_of(1, 3, 64, 5, 9, (24, 20, 20), 2)
