@@ -526,7 +526,7 @@ int window_attn_launch(const void *q, const unstep_cache_t *cache, int window, v
     if (gsk > sms) gsk = sms;
     if (gsk > p.w_tail) gsk = p.w_tail;
     // a piece of fewer than four key tiles costs more in its scratch slot and merge than it saves
-    // (8-bit caches: 72 queries over 144 keys 16.4 -> 14.3 us, 312 over 936 37 -> 31 us); the bf16
+    // (8-bit caches: 72 queries over 144 keys 16.4 -> 12.3 us, 312 over 936 37 -> 31 us); the bf16
     // schedule keeps its pieces, and with them its results' bits
     if (q8) {
       const long long most = static_cast<long long>(tail) * (p.n_tiles < 8 ? 1 : p.n_tiles / 4);
