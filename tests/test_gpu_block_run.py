@@ -135,6 +135,52 @@ def test_norms_around_the_projections(cuda_lib):
     assert all(torch.equal(a, b) for a, b in zip(*results))
 
 
+def test_inputs_from_another_stream(cuda_lib):
+    """Rows made on a side stream while the main stream's norms run, joined by an event, eagerly and
+    as a fork and join in a graph: no norm sees them before they are there."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(13)
+    rows, C = 3000, 512
+    src = torch.randn((rows, C), generator=g, device="cuda")
+    busy, x = torch.zeros((rows, C), device="cuda"), torch.zeros((rows, C), device="cuda")
+    n, side = Norm("layer", 1e-6), torch.cuda.Stream()
+    scratch = torch.empty_like(busy, dtype=BF)
+
+    def run(out):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            t = src
+            for _ in range(20):
+                t = t * 1.5 - src
+            x.copy_(t)
+        for _ in range(3):
+            binding.norm_modulate(busy, n, out=scratch)
+        main.wait_stream(side)
+        binding.norm_modulate(x, n, out=out)
+        # and back: the side stream overwrites the rows once the norm has read them
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            x.zero_()
+        main.wait_stream(side)
+
+    t = src
+    for _ in range(20):
+        t = t * 1.5 - src
+    want, out = binding.norm_modulate(t, n), torch.empty_like(scratch)
+    for _ in range(20):
+        out.zero_()
+        run(out)
+        assert torch.equal(out, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(out)
+    for _ in range(20):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, want)
+
+
 def test_block_in_a_graph(cuda_lib):
     """Three layers captured once and replayed on new inputs, against eager calls on a second set."""
     shape = shape_of(1, 3, 64, 5, 9, (24, 20, 20), 2)
