@@ -396,6 +396,8 @@ int unstep_cache_restore(unstep_cache_t *cache, const void *host_src, size_t byt
  * The conventions at the top of this file hold.  unstep_append_plan, unstep_window_plan,
  * unstep_cache_table_bytes, unstep_attn_scratch_bytes and unstep_get_device_error take &base; the
  * calls that read or write bf16 rows refuse it with UNSTEP_ERR_ARG once the cache is initialised.
+ * The kernels of this section and of the next may be set up while the stream's preceding kernel
+ * ends; they touch memory only once it has completed.
  * ------------------------------------------------------------------------------------------ */
 typedef struct {
   unstep_cache_t base; /* k_cache, v_cache: unstep_q8_cache_kv_bytes() bytes each */
