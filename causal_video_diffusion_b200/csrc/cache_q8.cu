@@ -21,6 +21,18 @@ constexpr int kThreads = 256;        // of the read-back
 constexpr int kAppendThreads = 128;  // six blocks an SM, 9 % faster for a chunk than two of 256
 constexpr uint32_t kFullMask = 0xFFFFFFFFu;
 
+// k and v, read once.  Not through the read-only path: the kernel is resident while its predecessor
+// may still write them, and q_out may be one of them, so the load is coherent and stays before the
+// thread's stores.
+__device__ __forceinline__ uint4 ld_once(const void *p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
 __device__ __forceinline__ void unpack8(const uint4 &w, float (&x)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -103,8 +115,8 @@ __global__ void __launch_bounds__(kAppendThreads, 6) q8_rope_kv_append_kernel(co
     qv[h] = kv[h] = vv[h] = make_uint4(0, 0, 0, 0);
     if (live) {
       qv[h] = ld_plain(static_cast<const __nv_bfloat16 *>(p.q) + m.e + h * de);
-      kv[h] = ld_stream(static_cast<const __nv_bfloat16 *>(p.k) + m.e + h * de);
-      vv[h] = ld_stream(static_cast<const __nv_bfloat16 *>(p.v) + m.e + h * de);
+      kv[h] = ld_once(static_cast<const __nv_bfloat16 *>(p.k) + m.e + h * de);
+      vv[h] = ld_once(static_cast<const __nv_bfloat16 *>(p.v) + m.e + h * de);
     }
   }
 #pragma unroll

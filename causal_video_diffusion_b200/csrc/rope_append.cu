@@ -28,6 +28,15 @@ constexpr int kThreads = 256;
 template <bool kQ>
 constexpr int items_per_thread() { return kQ ? UNSTEP_ROPE_ITEMS : UNSTEP_ROPE_ITEMS_KV; }
 
+// k and v, which no kernel writes while this one runs: it starts after its predecessors have ended.
+__device__ __forceinline__ uint4 ld_stream(const void *p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
 // kQ: q is rotated in place; without it q is neither read nor written.
 template <int D, bool kQ>
 __global__ void __launch_bounds__(kThreads) rope_kv_append_kernel(const RopeAppendParams p,

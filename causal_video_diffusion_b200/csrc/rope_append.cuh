@@ -8,14 +8,6 @@
 
 namespace unstep {
 
-__device__ __forceinline__ uint4 ld_stream(const void *p) {
-  uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
-  return r;
-}
-
 __device__ __forceinline__ uint4 ld_plain(const void *p) {
   return *reinterpret_cast<const uint4 *>(p);
 }
@@ -83,7 +75,7 @@ __device__ __forceinline__ bool locate(const RopeAppendParams &p, uint32_t it, I
     } else {
       src = p.tab_w + static_cast<int>(x) * p.half_w + (pr - p.half_t - p.half_h);
     }
-    m.cs[u] = __ldg(src);
+    m.cs[u] = __ldg(src);  // the tables are written by the cache's initialisation alone
   }
   return true;
 }

@@ -499,11 +499,20 @@ struct Decoder {
     src_lane = lane >> 2;
   }
 
-  // Scale bytes of this lane's row (1 behind `valid`).  src: the tile's scales.
+  // Scale bytes of this lane's row (1 behind `valid`).  src: the tile's scales.  Coherent loads, kept
+  // behind the wait for the predecessor: this grid is resident while the append that writes the
+  // scales may still run, which the read-only path does not allow.
   __device__ __forceinline__ uint32_t scales(const unsigned char *src, int valid) const {
     if (srow >= valid) return 0x7F7F7F7Fu;
-    return D == 128 ? __ldg(reinterpret_cast<const uint32_t *>(src + srow * kScales))
-                    : __ldg(reinterpret_cast<const uint16_t *>(src + srow * kScales));
+    uint32_t w;
+    if constexpr (D == 128) {
+      asm volatile("ld.global.u32 %0, [%1];" : "=r"(w) : "l"(src + srow * kScales) : "memory");
+    } else {
+      uint16_t h;
+      asm volatile("ld.global.u16 %0, [%1];" : "=h"(h) : "l"(src + srow * kScales) : "memory");
+      w = h;
+    }
+    return w;
   }
 
   // Decodes half tile `half` under the scales `word` into the swizzled bf16 tile `to` bytes behind
