@@ -84,33 +84,39 @@ long long attribute(PyObject *o, const char *name) {
 // A call's place: its device, made current for as long as this lives, and the stream.
 struct Place {
   int index;
-  PyObject *stream;  // None: the device's current stream
-  unstep_stream_t handle;
   c10::cuda::CUDAGuard guard;
+  c10::cuda::CUDAStream current, stream;  // the device's current stream; the call's
+  unstep_stream_t handle;
 
   Place(int device, PyObject *s)
-      : index(device), stream(s), guard(static_cast<c10::DeviceIndex>(device)) {
-    if (is_none(s)) {
-      handle = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
-    } else {
-      const long long at = attribute(s, "device_index");
-      if (at != device)
-        refuse("stream is on cuda:" + std::to_string(at) + ", the tensors on cuda:" +
-               std::to_string(device));
-      handle = reinterpret_cast<unstep_stream_t>(attribute(s, "cuda_stream"));
-    }
+      : index(device),
+        guard(static_cast<c10::DeviceIndex>(device)),
+        current(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device))),
+        stream(is_none(s) ? current : given(device, s)),
+        handle(stream.stream()) {}
+
+  static c10::cuda::CUDAStream given(int device, PyObject *s) {
+    const long long at = attribute(s, "device_index");
+    if (at != device)
+      refuse("stream is on cuda:" + std::to_string(at) + ", the tensors on cuda:" +
+             std::to_string(device));
+    return c10::cuda::CUDAStream(
+        c10::Stream::unpack3(attribute(s, "stream_id"), static_cast<c10::DeviceIndex>(at),
+                             static_cast<c10::DeviceType>(attribute(s, "device_type"))));
   }
 
-  // A new output that the call writes: its memory is not reused before the stream is done with it.
+  // A new output that the call writes on `stream`.  It comes from that stream's memory: a block of
+  // the current stream's may have been freed behind work there that still reads it, which the call
+  // would not wait for.  The caller goes on with it on the current stream, so it is recorded there.
   at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type) const {
-    at::Tensor t = at::empty(shape, at::TensorOptions(at::Device(at::kCUDA, index)).dtype(type));
-    if (!is_none(stream)) {
-      PyObject *o = THPVariable_Wrap(t), *r = o ? PyObject_CallMethod(o, "record_stream", "O", stream)
-                                                : nullptr;
-      Py_XDECREF(o);
-      if (!r) throw PythonError{};
-      Py_DECREF(r);
+    const auto options = at::TensorOptions(at::Device(at::kCUDA, index)).dtype(type);
+    if (stream == current) return at::empty(shape, options);
+    at::Tensor t;
+    {
+      const c10::cuda::CUDAStreamGuard on(stream);
+      t = at::empty(shape, options);
     }
+    t.record_stream(current);
     return t;
   }
 };
