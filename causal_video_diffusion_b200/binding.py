@@ -733,7 +733,8 @@ def norm_modulate(x: torch.Tensor, norm: Norm, out: Optional[torch.Tensor] = Non
     """``norm`` of every row of x (bf16 or fp32 ``[..., C]``, rows at one stride) as bf16.
 
     The norm and modulation before a DiT block, or with a weight alone the norm of projected
-    queries and keys.  ``out`` may be x itself when x is bf16.
+    queries and keys.  ``out`` may be x itself when x is bf16, but not share memory with x or the
+    norm's tensors otherwise (UnstepError).
     """
     return (_HOST or _host()).norm_modulate(x, norm, out, stream)
 
@@ -750,7 +751,8 @@ def gate_residual_norm(x: torch.Tensor, y: torch.Tensor, gate: Optional[torch.Te
     x: the residual stream, bf16 or fp32 ``[..., C]``; y: the block's output, bf16 of x's shape;
     gate: ``[G][C]`` as a Norm's scale, or None for 1.  ``x_out`` None updates x in place;
     ``next`` None leaves the second output out (None).  ``next`` sees the fp32 sum, before it is
-    rounded to x's type.  Returns (x_out, out).
+    rounded to x's type.  Outputs that share memory with another tensor of the call (but for x_out
+    that is x) are refused (UnstepError).  Returns (x_out, out).
     """
     return (_HOST or _host()).gate_residual_norm(x, y, gate, res_scale, post, next, x_out, out,
                                                  stream)

@@ -1048,6 +1048,51 @@ bool bad_stride(long long ld, long long rows, int C) {
   return (ld & 7) || ld < 0 || (rows > 1 && ld < C);
 }
 
+// `rows` rows of `bytes` bytes, `stride` bytes apart (none: at is NULL).
+struct RowSet {
+  uintptr_t at;
+  long long rows, stride, bytes;
+
+  RowSet(const void *p, int type, long long ld, long long n, int C)
+      : at(reinterpret_cast<uintptr_t>(p)), rows(n), stride(ld * width(type)), bytes(C * width(type)) {
+    if (rows > 1 && stride <= bytes) {  // one piece (rows of parameters may even lie on each other)
+      bytes += (rows - 1) * stride;
+      rows = 1;
+    }
+  }
+  static long long width(int type) { return type == UNSTEP_F32 ? 4 : 2; }
+  uintptr_t end() const { return at + static_cast<uintptr_t>((rows - 1) * stride + bytes); }
+};
+
+// Whether row i of a shares a byte with a row of b.
+bool row_meets(const RowSet &a, long long i, const RowSet &b) {
+  const long long d = static_cast<long long>(a.at - b.at) + i * a.stride;  // from b's first row
+  if (d + a.bytes <= 0) return false;
+  if (b.rows == 1) return d < b.bytes;
+  const long long j = d < b.bytes ? 0 : (d - b.bytes) / b.stride + 1;  // b's first row to end after d
+  return j < b.rows && j * b.stride < d + a.bytes;
+}
+
+// Whether two sets share a byte.  Sets of one stride (column blocks of a wider tensor) share one
+// where the first row of either is in it: a meeting pair of later rows moves back to one.
+bool share(const RowSet &a, const RowSet &b) {
+  if (!a.at || !b.at || a.end() <= b.at || b.end() <= a.at) return false;
+  if (a.rows > b.rows) return share(b, a);
+  if (row_meets(a, 0, b) || row_meets(b, 0, a)) return true;
+  if (a.rows > 1 && a.stride == b.stride) return false;
+  for (long long i = 1; i < a.rows; ++i)
+    if (row_meets(a, i, b)) return true;
+  return false;
+}
+
+// Whether an output shares a byte with a norm's parameters for `groups` groups.
+bool shares_parameters(const RowSet &out, const unstep_norm_t &n, long long groups, int C) {
+  const int t = n.param_type;
+  return share(out, {n.weight, t, 0, 1, C}) || share(out, {n.bias, t, 0, 1, C}) ||
+         share(out, {n.scale, t, n.mod_stride, groups, C}) ||
+         share(out, {n.shift, t, n.mod_stride, groups, C});
+}
+
 }  // namespace
 
 extern "C" {
@@ -1064,7 +1109,13 @@ int unstep_norm_modulate(const void *x, int x_type, long long ldx, void *y, long
   if (!x || !y) return UNSTEP_ERR_ARG;
   if (bad_stride(ldx, rows, C) || bad_stride(ldy, rows, C)) return UNSTEP_ERR_SHAPE;
   if (!aligned16(x) || !aligned16(y)) return UNSTEP_ERR_ALIGN;
-  if (y == x && (x_type != UNSTEP_BF16 || ldy != ldx)) return UNSTEP_ERR_ARG;
+  // the rows run in no order, and one is loaded while the one before it is stored
+  const long long groups = (rows - 1) / rows_per_group + 1;
+  const RowSet out(y, UNSTEP_BF16, ldy, rows, C);
+  const bool onto_x = y == x && x_type == UNSTEP_BF16 && ldy == ldx;
+  if ((!onto_x && (y == x || share(out, {x, x_type, ldx, rows, C}))) ||
+      shares_parameters(out, *norm, groups, C))
+    return UNSTEP_ERR_ARG;
   unstep::NormParams p{};
   p.x = x;
   p.x_type = x_type;
@@ -1103,8 +1154,17 @@ int unstep_gate_residual_norm(const void *x, int x_type, long long ldx, const vo
     return UNSTEP_ERR_SHAPE;
   if (!aligned16(x) || !aligned16(y) || !aligned16(gate) || !aligned16(x_out) || !aligned16(h))
     return UNSTEP_ERR_ALIGN;
-  if ((x_out == x && ldxo != ldx) || h == x || h == y || h == x_out || x_out == y)
+  const long long groups = (rows - 1) / rows_per_group + 1;
+  const RowSet x_set(x, x_type, ldx, rows, C), y_set(y, UNSTEP_BF16, ldy, rows, C);
+  const RowSet sum_set(x_out, x_type, ldxo, rows, C), h_set(h, UNSTEP_BF16, ldh, rows, C);
+  if ((x_out == x ? ldxo != ldx : share(sum_set, x_set)) || share(h_set, x_set) ||
+      share(h_set, sum_set))
     return UNSTEP_ERR_ARG;
+  for (const RowSet *out : {&sum_set, &h_set})
+    if (share(*out, y_set) || share(*out, {gate, gate_type, gate_stride, groups, C}) ||
+        (post && shares_parameters(*out, *post, groups, C)) ||
+        (next && shares_parameters(*out, *next, groups, C)))
+      return UNSTEP_ERR_ARG;
   unstep::NormParams p{};
   p.x = x;
   p.x_type = x_type;

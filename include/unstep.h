@@ -485,8 +485,9 @@ typedef struct {
  * alone, the norm of projected queries and keys).  x is bf16 or fp32 (x_type), y bf16 (RNE, one
  * rounding).  Row strides ldx, ldy in elements, so x may be a column block of a wider tensor.
  * C a multiple of 8, 8 <= C <= 16384; strides and mod_stride multiples of 8, ldx, ldy >= C when
- * rows > 1; all pointers 16-byte aligned.  y may alias x when x is bf16 and ldy == ldx; no other
- * overlap.  rows == 0 does nothing.
+ * rows > 1; all pointers 16-byte aligned.  y may be x itself when x is bf16 and ldy == ldx; rows of y
+ * that share a byte with x or the norm's parameters otherwise are refused (ARG); column blocks of one
+ * wider tensor share none.  rows == 0 does nothing.
  * Errors: ARG, SHAPE, ALIGN, UNSUPPORTED (C > 16384), CUDA.
  */
 int unstep_norm_modulate(const void *x, int x_type, long long ldx, void *y, long long ldy,
@@ -499,7 +500,8 @@ int unstep_norm_modulate(const void *x, int x_type, long long ldx, void *y, long
  *   h[r]     = next(x[r] + res_scale * gate_g * post(y[r]))      (from the fp32 sum, not x_out)
  * x and x_out are bf16 or fp32 (x_type), y and h bf16.  gate: group g's C elements at element
  * g * gate_stride, of type gate_type (NULL: 1).  post NULL: y itself.  next NULL: h is not
- * computed (h must be NULL too).  x_out may be x itself with ldxo == ldx; no other overlap.
+ * computed (h must be NULL too).  x_out may be x itself with ldxo == ldx; rows of x_out or h that
+ * share a byte with each other or with an input otherwise are refused (ARG).
  * Sizes, strides, groups, alignment and errors as in unstep_norm_modulate.
  */
 int unstep_gate_residual_norm(const void *x, int x_type, long long ldx, const void *y,
