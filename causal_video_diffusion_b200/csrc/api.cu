@@ -428,6 +428,25 @@ int unstep_window_plan(const unstep_cache_t *cache, int window, unstep_window_pl
 
 namespace {
 
+// Whether `na` bytes at a and `nb` at b share one (a NULL shares none).
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x && y && (x < y ? y - x < na : x - y < nb);
+}
+
+// Whether `bytes` at p share one with an 8-bit cache's codes or scales.
+bool overlaps_rows(const void *p, size_t bytes, const unstep_q8_cache_t *c) {
+  const size_t codes = unstep_q8_cache_kv_bytes(c), scales = unstep_q8_cache_scale_bytes(c);
+  return overlap(p, bytes, c->base.k_cache, codes) || overlap(p, bytes, c->base.v_cache, codes) ||
+         overlap(p, bytes, c->k_scale, scales) || overlap(p, bytes, c->v_scale, scales);
+}
+
+// Bytes of a tensor of `rows` tokens' activations.
+size_t act_bytes(const unstep_cache_t *c, long long rows) {
+  return 2ull * static_cast<size_t>(act_B(c)) * static_cast<size_t>(rows) *
+         static_cast<size_t>(act_H(c)) * static_cast<size_t>(c->D);
+}
+
 // What unstep_window_attn_ex and unstep_window_attn_noalloc share: validation, the window plan,
 // the tensor maps, the persistent schedule and the launch.  `fixed_buffer` selects the scratch:
 // false, the cache's own (cache->attn_scratch, sized at unstep_cache_init; none: one CTA per
@@ -448,6 +467,10 @@ int window_attn_launch(const void *q, const unstep_cache_t *cache, int window, v
   const int tf = cache->Hg * cache->Wg;
   const int L = cache->last_chunk_frames * tf;
   const long long R = static_cast<long long>(cache->cap_frames) * tf;
+  // a unit's rows are written while other CTAs may still load its queries or the cache
+  if (q8 && (overlap(out, act_bytes(cache, L), q, act_bytes(cache, L)) ||
+             overlaps_rows(out, act_bytes(cache, L), q8)))
+    return UNSTEP_ERR_ARG;
   const int n_pairs = (L + 255) / 256;
   // (head, 256-query) units are numbered in int32 by the kernel
   const long long units = static_cast<long long>(B) * H * n_pairs;
@@ -826,12 +849,6 @@ int check_ready_q8(const unstep_q8_cache_t *c) {
   return UNSTEP_OK;
 }
 
-// Whether two ranges of `bytes` bytes share one.
-bool overlap(const void *a, const void *b, size_t bytes) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y ? y - x < bytes : x - y < bytes;
-}
-
 // Ring rows of `count` frames from frame f0 on: at most two ranges.
 void ring_rows(const unstep_cache_t *c, int f0, int count, int (&row)[2], int (&len)[2]) {
   const int tf = c->Hg * c->Wg, s0 = f0 % c->cap_frames;
@@ -889,10 +906,10 @@ int unstep_q8_rope_kv_append(const void *q, void *q_out, const void *k, const vo
     return UNSTEP_ERR_UNSUPPORTED;
   // a thread reads its elements of q, k and v before it writes those of q_out: q_out may be one of
   // them, but not lie across one
-  const size_t chunk = 2ull * static_cast<size_t>(act_B(c)) * static_cast<size_t>(rows) *
-                       static_cast<size_t>(act_H(c)) * static_cast<size_t>(c->D);
+  const size_t chunk = act_bytes(c, rows);
   for (const void *in : {q, k, v})
-    if (in != q_out && overlap(q_out, in, chunk)) return UNSTEP_ERR_ARG;
+    if (in != q_out && overlap(q_out, chunk, in, chunk)) return UNSTEP_ERR_ARG;
+  if (overlaps_rows(q_out, chunk, cache)) return UNSTEP_ERR_ARG;
   unstep::Q8AppendParams p{};
   p.rope = append_params(c, k, v, frame_idx, grid);
   p.rope.q = const_cast<void *>(q);  // read only
@@ -928,6 +945,11 @@ int unstep_q8_cache_read(const unstep_q8_cache_t *cache, int first_frame, int fr
   if (c->last_chunk_frames < 1 || first_frame < c->first_frame || end > c->frames_written ||
       first_frame < c->frames_written - c->cap_frames)
     return UNSTEP_ERR_WINDOW;
+  const size_t out = 2ull * static_cast<size_t>(c->B) * c->H * static_cast<size_t>(frames) * c->Hg *
+                     c->Wg * static_cast<size_t>(c->D);
+  if (overlap(k_out, out, v_out, out) || overlaps_rows(k_out, out, cache) ||
+      overlaps_rows(v_out, out, cache))
+    return UNSTEP_ERR_ARG;
   unstep::Q8ReadParams p{};
   p.k_cache = static_cast<const unsigned char *>(c->k_cache);
   p.v_cache = static_cast<const unsigned char *>(c->v_cache);

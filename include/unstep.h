@@ -416,8 +416,9 @@ int unstep_q8_cache_init(unstep_q8_cache_t *cache, unstep_stream_t stream);
 /*
  * unstep_rope_kv_append into an 8-bit cache: k is rotated and v copied, both are quantised as
  * they are written.  The rotated queries go to q_out, bf16 in q's layout; q_out == q rotates in
- * place.  q_out may be q, k or v itself, but not overlap one of them otherwise (ARG).  For a shard cache only the shard's streams and heads
- * of q_out are written.  Frame order, slots and metadata as in unstep_rope_kv_append.
+ * place.  q_out may be q, k or v itself, but not overlap one of them otherwise, nor the cache (ARG).
+ * For a shard cache only the shard's streams and heads of q_out are written.  Frame order, slots and
+ * metadata as in unstep_rope_kv_append.
  * Errors: those of unstep_rope_kv_append, plus UNSUPPORTED for 2^31 or more 8-channel vectors in
  * the chunk.
  */
@@ -429,7 +430,7 @@ int unstep_q8_rope_kv_append(const void *q, void *q_out, const void *k, const vo
  * unstep_window_attn over an 8-bit cache: softmax attention of the latest chunk's rotated queries
  * over the stored values of the window's rows, bf16 tensor-core products with fp32 accumulation
  * and fp32 online softmax, output rounded to bf16 (RNE).  Rows outside the window are not read.
- * Errors: those of unstep_window_attn.
+ * Errors: those of unstep_window_attn; ARG also for an out that overlaps q or the cache.
  */
 int unstep_q8_window_attn(const void *q, const unstep_q8_cache_t *cache, int window, void *out,
                           unstep_stream_t stream);
@@ -438,7 +439,8 @@ int unstep_q8_window_attn(const void *q, const unstep_q8_cache_t *cache, int win
  * Reads frames first_frame .. first_frame+frames-1 back, in time order, as bf16
  * [B][H][frames*Hg*Wg][D] into k_out and v_out (either may be NULL, not both).  The values are
  * exact (see above); K is the rotated K.  The frames must be in the ring: not before the stream's
- * first frame, not after the newest one, and among the last cap_frames.
+ * first frame, not after the newest one, and among the last cap_frames.  The outputs may overlap
+ * neither each other nor the cache (ARG).
  * Errors: ARG, ALIGN, WINDOW (a frame that the ring does not hold), CUDA.
  */
 int unstep_q8_cache_read(const unstep_q8_cache_t *cache, int first_frame, int frames, void *k_out,

@@ -33,3 +33,16 @@ def test_rotated_queries_onto_k_or_v(cuda_lib, D, split, H, onto):
         assert torch.equal(over, want) and torch.equal(out, want_out)
         for name in ("k_codes", "v_codes", "k_scale", "v_scale"):
             assert torch.equal(getattr(cache, name).view(torch.uint8), getattr(twin, name).view(torch.uint8))
+
+
+def test_attention_onto_its_queries_is_refused(cuda_lib):
+    shape = shape_of(1, 2, 64, 4, 6, (24, 20, 20), 1)
+    cache = R.make_cache(shape, 2, 4)
+    q, k, v = draw(shape, 3)
+    cache.rope_kv_append(q, k, v, 0, 1)
+    for f in (lambda: cache.window_attn(q, 1, out=q),
+              lambda: cache.read_frames(0, 1, k_out=(t := torch.empty((1, 2, 24, 64), dtype=q.dtype,
+                                                                      device="cuda")), v_out=t)):
+        with pytest.raises(binding.UnstepError) as e:
+            f()
+        assert e.value.status == binding.UNSTEP_ERR_ARG
