@@ -902,7 +902,8 @@ int unstep_q8_rope_kv_append(const void *q, void *q_out, const void *k, const vo
   const int is_new = unstep_append_plan(c, frame_idx, grid, nullptr);
   if (is_new < 0) return is_new;
   const long long rows = static_cast<long long>(grid.frames) * c->Hg * c->Wg;
-  if (rows > INT_MAX || static_cast<long long>(c->B) * c->H > (1ll << 31) / (c->D / 8) / rows - 1)
+  // the kernel numbers the chunk's 8-channel vectors in 31 bits (rows <= 2^30, so nothing overflows)
+  if (static_cast<long long>(c->B) * c->H > ((1ll << 31) - 1) / (rows * (c->D / 8)))
     return UNSTEP_ERR_UNSUPPORTED;
   // a thread reads its elements of q, k and v before it writes those of q_out: q_out may be one of
   // them, but not lie across one

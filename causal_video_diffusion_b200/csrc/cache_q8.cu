@@ -203,7 +203,7 @@ cudaError_t launch_q8_rope_kv_append(const Q8AppendParams &in, cudaStream_t stre
   if (r.D != 128 && r.D != 64) return cudaErrorInvalidValue;
   const int heads = r.H % 4 == 0 ? 4 : r.H % 3 == 0 ? 3 : r.H % 2 == 0 ? 2 : 1;
   const long long n_items = static_cast<long long>(r.B) * r.L * (r.H / heads) * (r.D / 8);
-  if (n_items < 1 || n_items >= (1ll << 31) - kAppendThreads) return cudaErrorInvalidConfiguration;
+  if (n_items < 1 || n_items >= (1ll << 31)) return cudaErrorInvalidConfiguration;
   r.slot0 = r.frame_idx % r.cap;
   r.div_h = make_fastdiv(static_cast<uint32_t>(r.H / heads));
   r.div_l = make_fastdiv(static_cast<uint32_t>(r.L));
