@@ -37,8 +37,9 @@ __device__ __forceinline__ float q8_inv_scale(uint32_t byte) {
   return __uint_as_float((254u - byte) << 23);
 }
 
-// Two values -> two codes (lo in the low byte).  |x * inv| <= 448, but under the top scale byte up
-// to 512: there the caller clamps to 240 first, since 256 * 2^120 would already be infinite.
+// Two values -> two codes (lo in the low byte).  |x * inv| <= 448; under the top scale byte (2^120)
+// below 256, as fp32 ends at 2^128.  There the caller clamps to 240 first: a value that rounds up to
+// the code 256 would read back as 2^128, which is infinite.
 __device__ __forceinline__ uint32_t q8_encode2(float lo, float hi, float inv) {
   const uint64_t inv2 = f2_make(inv, inv);
   float a, b;
