@@ -5,7 +5,8 @@
 // kernels take 4 microseconds; marshalling them through Python objects took 6 to 15 (checks of nine
 // tensors, a structure for each norm, eighteen converted arguments), here it is about one.  Argument
 // errors become ValueError, the ABI's status codes the UnstepError that bind() was given.  Nothing
-// is kept between calls.
+// but what bind() was given is kept between calls, and that by each module object for itself: a second
+// instance of the binding, on another build of the library, does not reach the first one's calls.
 #include <Python.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -20,15 +21,15 @@
 
 namespace {
 
-// The library's entry points and the exception of its status codes, from bind().
-struct {
+// A module object's own: the library's entry points and the exception of its status codes, from bind().
+struct Library {
   decltype(&unstep_norm_modulate) norm_modulate;
   decltype(&unstep_gate_residual_norm) gate_residual_norm;
   decltype(&unstep_q8_rope_kv_append) append;
   decltype(&unstep_q8_window_attn) attn;
   decltype(&unstep_q8_cache_read) read;
-} lib;
-PyObject *unstep_error = nullptr;
+  PyObject *error;
+};
 
 struct BadArgument {
   std::string what;
@@ -36,6 +37,12 @@ struct BadArgument {
 struct PythonError {};  // already set
 
 [[noreturn]] void refuse(const std::string &what) { throw BadArgument{what}; }
+
+const Library &library(PyObject *module) {
+  const Library *l = static_cast<const Library *>(PyModule_GetState(module));
+  if (!l->error) refuse("bind() comes before any call");
+  return *l;
+}
 
 std::string shape_text(at::IntArrayRef s) {
   std::string t = "(";
@@ -121,11 +128,11 @@ struct Place {
   }
 };
 
-void check(int status, const char *name) {
+void check(const Library &lib, int status, const char *name) {
   if (status >= 0) return;
-  PyObject *e = PyObject_CallFunction(unstep_error, "is", status, name);
+  PyObject *e = PyObject_CallFunction(lib.error, "is", status, name);
   if (e) {
-    PyErr_SetObject(unstep_error, e);
+    PyErr_SetObject(lib.error, e);
     Py_DECREF(e);
   }
   throw PythonError{};
@@ -278,26 +285,29 @@ Output output(PyObject *o, const at::Tensor &x, at::ScalarType type, const char 
 }
 
 // (x, norm, out, stream) -> out
-PyObject *norm_modulate(PyObject *, PyObject *const *a, Py_ssize_t n) {
+PyObject *norm_modulate(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
     if (n != 4) refuse("norm_modulate takes four arguments");
+    const Library &lib = library(self);
     const at::Tensor &x = tensor(a[0], "x");
     Rows xr;
     Batch b = batch_of(x, xr);
     const unstep_norm_t spec = norm_of(a[1], b);
     const Place at(b.index, a[3]);
     const Output out = output(a[2], x, at::kBFloat16, "out", at);
-    check(lib.norm_modulate(x.data_ptr(), type_code(x), xr.ld, out.t.data_ptr(), out.ld, b.rows,
-                            static_cast<int>(b.C), b.per_group(), &spec, at.handle),
-          "unstep_norm_modulate");
+    const int status =
+        lib.norm_modulate(x.data_ptr(), type_code(x), xr.ld, out.t.data_ptr(), out.ld, b.rows,
+                          static_cast<int>(b.C), b.per_group(), &spec, at.handle);
+    check(lib, status, "unstep_norm_modulate");
     return out.release();
   });
 }
 
 // (x, y, gate, res_scale, post, next, x_out, out, stream) -> (x_out, out)
-PyObject *gate_residual_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
+PyObject *gate_residual_norm(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
     if (n != 9) refuse("gate_residual_norm takes nine arguments");
+    const Library &lib = library(self);
     const at::Tensor &x = tensor(a[0], "x");
     Rows xr;
     Batch b = batch_of(x, xr);
@@ -323,12 +333,12 @@ PyObject *gate_residual_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                     : output(a[6], x, x.scalar_type(), "x_out", at);
     Output out{{}, Py_None, 0};
     if (!is_none(a[5])) out = output(a[7], x, at::kBFloat16, "out", at);
-    check(lib.gate_residual_norm(x.data_ptr(), type_code(x), xr.ld, y.data_ptr(), yr.ld, gate.p,
-                                 gate_type, gate.stride, res_scale, is_none(a[4]) ? nullptr : &post,
-                                 is_none(a[5]) ? nullptr : &next, xo.t.data_ptr(), xo.ld,
-                                 is_none(a[5]) ? nullptr : out.t.data_ptr(), out.ld, b.rows,
-                                 static_cast<int>(b.C), b.per_group(), at.handle),
-          "unstep_gate_residual_norm");
+    const int status = lib.gate_residual_norm(
+        x.data_ptr(), type_code(x), xr.ld, y.data_ptr(), yr.ld, gate.p, gate_type, gate.stride,
+        res_scale, is_none(a[4]) ? nullptr : &post, is_none(a[5]) ? nullptr : &next,
+        xo.t.data_ptr(), xo.ld, is_none(a[5]) ? nullptr : out.t.data_ptr(), out.ld, b.rows,
+        static_cast<int>(b.C), b.per_group(), at.handle);
+    check(lib, status, "unstep_gate_residual_norm");
     PyObject *first = xo.release(), *second = first ? out.release() : nullptr;
     if (!second) {
       Py_XDECREF(first);
@@ -372,9 +382,10 @@ struct Cache {
 };
 
 // (cache, device, q, k, v, frame_idx, frames, q_out, stream) -> q_out
-PyObject *q8_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
+PyObject *q8_append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
     if (n != 9) refuse("q8_append takes nine arguments");
+    const Library &lib = library(self);
     const Cache c(a[0], a[1]);
     const long long first = integer(a[5], "frame_idx"), frames = integer(a[6], "frames");
     const void *q = c.activation(a[2], frames, "q");
@@ -383,16 +394,17 @@ PyObject *q8_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     void *q_out = c.activation(out, frames, "q_out");
     const Place at(c.index, a[8]);
     const unstep_grid_t grid{static_cast<int>(frames), c.q8->base.Hg, c.q8->base.Wg};
-    check(lib.append(q, q_out, k, v, c.q8, static_cast<int>(first), grid, at.handle),
-          "unstep_q8_rope_kv_append");
+    const int status = lib.append(q, q_out, k, v, c.q8, static_cast<int>(first), grid, at.handle);
+    check(lib, status, "unstep_q8_rope_kv_append");
     return same(out);
   });
 }
 
 // (cache, device, q, window, out, stream) -> out
-PyObject *q8_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
+PyObject *q8_attn(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
     if (n != 6) refuse("q8_attn takes six arguments");
+    const Library &lib = library(self);
     const Cache c(a[0], a[1]);
     const int frames = c.q8->base.last_chunk_frames;
     const void *q = c.activation(a[2], frames, "q");
@@ -406,21 +418,23 @@ PyObject *q8_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
     } else {
       out = c.activation(a[4], frames, "out");
     }
-    check(lib.attn(q, c.q8, static_cast<int>(window), out, at.handle), "unstep_q8_window_attn");
+    const int status = lib.attn(q, c.q8, static_cast<int>(window), out, at.handle);
+    check(lib, status, "unstep_q8_window_attn");
     return is_none(a[4]) ? THPVariable_Wrap(fresh) : same(a[4]);
   });
 }
 
 // (cache, device, first_frame, frames, k_out, v_out, stream) -> (k, v)
-PyObject *q8_read(PyObject *, PyObject *const *a, Py_ssize_t n) {
+PyObject *q8_read(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
     if (n != 7) refuse("q8_read takes seven arguments");
+    const Library &lib = library(self);
     const Cache c(a[0], a[1]);
     const unstep_cache_t &base = c.q8->base;
     const long long first = integer(a[2], "first_frame"), frames = integer(a[3], "frames");
     // before any output is made
     if (frames < 1 || frames > base.cap_frames)
-      check(frames < 1 ? UNSTEP_ERR_ARG : UNSTEP_ERR_WINDOW, "unstep_q8_cache_read");
+      check(lib, frames < 1 ? UNSTEP_ERR_ARG : UNSTEP_ERR_WINDOW, "unstep_q8_cache_read");
     const int64_t want[4] = {base.B, base.H, frames * base.Hg * base.Wg, base.D};
     const Place at(c.index, a[6]);
     at::Tensor outs[2];
@@ -437,9 +451,9 @@ PyObject *q8_read(PyObject *, PyObject *const *a, Py_ssize_t n) {
                shape_text(at::IntArrayRef(want, 4)) + " on cuda:" + std::to_string(c.index));
       outs[i] = t;
     }
-    check(lib.read(c.q8, static_cast<int>(first), static_cast<int>(frames), outs[0].data_ptr(),
-                   outs[1].data_ptr(), at.handle),
-          "unstep_q8_cache_read");
+    const int status = lib.read(c.q8, static_cast<int>(first), static_cast<int>(frames),
+                                outs[0].data_ptr(), outs[1].data_ptr(), at.handle);
+    check(lib, status, "unstep_q8_cache_read");
     PyObject *k = is_none(a[4]) ? THPVariable_Wrap(outs[0]) : same(a[4]);
     PyObject *v = !k ? nullptr : is_none(a[5]) ? THPVariable_Wrap(outs[1]) : same(a[5]);
     PyObject *pair = v ? PyTuple_Pack(2, k, v) : nullptr;
@@ -450,7 +464,7 @@ PyObject *q8_read(PyObject *, PyObject *const *a, Py_ssize_t n) {
 }
 
 // (UnstepError, addresses of the five entry points)
-PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
+PyObject *bind(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   if (n != 6) {
     PyErr_SetString(PyExc_TypeError, "bind takes six arguments");
     return nullptr;
@@ -461,12 +475,14 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind: a null entry point");
       return nullptr;
     }
-  lib = {reinterpret_cast<decltype(lib.norm_modulate)>(p[0]),
-         reinterpret_cast<decltype(lib.gate_residual_norm)>(p[1]),
-         reinterpret_cast<decltype(lib.append)>(p[2]), reinterpret_cast<decltype(lib.attn)>(p[3]),
-         reinterpret_cast<decltype(lib.read)>(p[4])};
+  Library *l = static_cast<Library *>(PyModule_GetState(self));
   Py_INCREF(a[0]);
-  Py_XSETREF(unstep_error, a[0]);
+  PyObject *old = l->error;
+  *l = {reinterpret_cast<decltype(l->norm_modulate)>(p[0]),
+        reinterpret_cast<decltype(l->gate_residual_norm)>(p[1]),
+        reinterpret_cast<decltype(l->append)>(p[2]), reinterpret_cast<decltype(l->attn)>(p[3]),
+        reinterpret_cast<decltype(l->read)>(p[4]), a[0]};
+  Py_XDECREF(old);
   Py_RETURN_NONE;
 }
 
@@ -475,9 +491,20 @@ PyMethodDef methods[] = {UNSTEP_METHOD(bind),      UNSTEP_METHOD(norm_modulate),
                          UNSTEP_METHOD(gate_residual_norm), UNSTEP_METHOD(q8_append),
                          UNSTEP_METHOD(q8_attn),   UNSTEP_METHOD(q8_read),
                          {nullptr, nullptr, 0, nullptr}};
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_host_calls", nullptr, -1, methods,
-                      nullptr, nullptr, nullptr, nullptr};
+int traverse(PyObject *m, visitproc visit, void *arg) {
+  if (const Library *l = static_cast<const Library *>(PyModule_GetState(m))) Py_VISIT(l->error);
+  return 0;
+}
+
+int clear(PyObject *m) {
+  if (Library *l = static_cast<Library *>(PyModule_GetState(m))) Py_CLEAR(l->error);
+  return 0;
+}
+
+PyModuleDef_Slot slots[] = {{0, nullptr}};  // multi-phase: a state for every module object
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_host_calls", nullptr, sizeof(Library), methods, slots,
+                      traverse, clear, nullptr};
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__host_calls() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__host_calls() { return PyModuleDef_Init(&module); }
