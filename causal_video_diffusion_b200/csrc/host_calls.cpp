@@ -44,6 +44,17 @@ const Library &library(PyObject *module) {
   return *l;
 }
 
+// Other Python threads run while this lives: an allocation or a launch may wait for the device, and
+// what the device waits for may be a host function that needs the interpreter.
+class Unlocked {
+  PyThreadState *state = PyEval_SaveThread();
+
+ public:
+  Unlocked() = default;
+  Unlocked(const Unlocked &) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 std::string shape_text(at::IntArrayRef s) {
   std::string t = "(";
   for (size_t i = 0; i < s.size(); ++i) t += (i ? ", " : "") + std::to_string(s[i]);
@@ -117,6 +128,7 @@ struct Place {
   // would not wait for.  The caller goes on with it on the current stream, so it is recorded there.
   at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type) const {
     const auto options = at::TensorOptions(at::Device(at::kCUDA, index)).dtype(type);
+    const Unlocked others;
     if (stream == current) return at::empty(shape, options);
     at::Tensor t;
     {
@@ -149,6 +161,13 @@ PyObject *guarded(F f) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
   }
   return nullptr;
+}
+
+// A library call's status, the interpreter unlocked meanwhile.
+template <class F, class... Args>
+int call(F f, Args... args) {
+  const Unlocked others;
+  return f(args...);
 }
 
 PyObject *same(PyObject *o) {
@@ -296,8 +315,8 @@ PyObject *norm_modulate(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     const Place at(b.index, a[3]);
     const Output out = output(a[2], x, at::kBFloat16, "out", at);
     const int status =
-        lib.norm_modulate(x.data_ptr(), type_code(x), xr.ld, out.t.data_ptr(), out.ld, b.rows,
-                          static_cast<int>(b.C), b.per_group(), &spec, at.handle);
+        call(lib.norm_modulate, x.data_ptr(), type_code(x), xr.ld, out.t.data_ptr(), out.ld, b.rows,
+             static_cast<int>(b.C), b.per_group(), &spec, at.handle);
     check(lib, status, "unstep_norm_modulate");
     return out.release();
   });
@@ -333,9 +352,9 @@ PyObject *gate_residual_norm(PyObject *self, PyObject *const *a, Py_ssize_t n) {
                                     : output(a[6], x, x.scalar_type(), "x_out", at);
     Output out{{}, Py_None, 0};
     if (!is_none(a[5])) out = output(a[7], x, at::kBFloat16, "out", at);
-    const int status = lib.gate_residual_norm(
-        x.data_ptr(), type_code(x), xr.ld, y.data_ptr(), yr.ld, gate.p, gate_type, gate.stride,
-        res_scale, is_none(a[4]) ? nullptr : &post, is_none(a[5]) ? nullptr : &next,
+    const int status = call(
+        lib.gate_residual_norm, x.data_ptr(), type_code(x), xr.ld, y.data_ptr(), yr.ld, gate.p,
+        gate_type, gate.stride, res_scale, is_none(a[4]) ? nullptr : &post, is_none(a[5]) ? nullptr : &next,
         xo.t.data_ptr(), xo.ld, is_none(a[5]) ? nullptr : out.t.data_ptr(), out.ld, b.rows,
         static_cast<int>(b.C), b.per_group(), at.handle);
     check(lib, status, "unstep_gate_residual_norm");
@@ -394,7 +413,8 @@ PyObject *q8_append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     void *q_out = c.activation(out, frames, "q_out");
     const Place at(c.index, a[8]);
     const unstep_grid_t grid{static_cast<int>(frames), c.q8->base.Hg, c.q8->base.Wg};
-    const int status = lib.append(q, q_out, k, v, c.q8, static_cast<int>(first), grid, at.handle);
+    const int status =
+        call(lib.append, q, q_out, k, v, c.q8, static_cast<int>(first), grid, at.handle);
     check(lib, status, "unstep_q8_rope_kv_append");
     return same(out);
   });
@@ -418,7 +438,7 @@ PyObject *q8_attn(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     } else {
       out = c.activation(a[4], frames, "out");
     }
-    const int status = lib.attn(q, c.q8, static_cast<int>(window), out, at.handle);
+    const int status = call(lib.attn, q, c.q8, static_cast<int>(window), out, at.handle);
     check(lib, status, "unstep_q8_window_attn");
     return is_none(a[4]) ? THPVariable_Wrap(fresh) : same(a[4]);
   });
@@ -451,8 +471,8 @@ PyObject *q8_read(PyObject *self, PyObject *const *a, Py_ssize_t n) {
                shape_text(at::IntArrayRef(want, 4)) + " on cuda:" + std::to_string(c.index));
       outs[i] = t;
     }
-    const int status = lib.read(c.q8, static_cast<int>(first), static_cast<int>(frames),
-                                outs[0].data_ptr(), outs[1].data_ptr(), at.handle);
+    const int status = call(lib.read, c.q8, static_cast<int>(first), static_cast<int>(frames),
+                            outs[0].data_ptr(), outs[1].data_ptr(), at.handle);
     check(lib, status, "unstep_q8_cache_read");
     PyObject *k = is_none(a[4]) ? THPVariable_Wrap(outs[0]) : same(a[4]);
     PyObject *v = !k ? nullptr : is_none(a[5]) ? THPVariable_Wrap(outs[1]) : same(a[5]);
