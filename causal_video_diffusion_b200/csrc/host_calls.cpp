@@ -10,11 +10,11 @@
 #include <Python.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
 
-#include <exception>
 #include <string>
 
 #include "../../include/unstep.h"
@@ -150,17 +150,18 @@ void check(const Library &lib, int status, const char *name) {
   throw PythonError{};
 }
 
+// torch's own errors (out of memory, a device error) become the exceptions that torch raises for them.
 template <class F>
 PyObject *guarded(F f) {
+  HANDLE_TH_ERRORS
   try {
     return f();
   } catch (const PythonError &) {
   } catch (const BadArgument &e) {
     PyErr_SetString(PyExc_ValueError, e.what.c_str());
-  } catch (const std::exception &e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
   }
   return nullptr;
+  END_HANDLE_TH_ERRORS
 }
 
 // A library call's status, the interpreter unlocked meanwhile.

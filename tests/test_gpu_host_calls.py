@@ -1,4 +1,4 @@
-"""The native side of the binding beside other threads."""
+"""The native side of the binding beside other threads, and its errors."""
 import ctypes
 import threading
 import time
@@ -71,3 +71,20 @@ def test_two_threads_with_caches_of_their_own(cuda_lib):
         t.join()
     for a, b in zip(alone, together):
         assert len(a) == len(b) == 90 and all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_out_of_memory_is_torchs_exception(cuda_lib):
+    """An output that does not fit raises torch.OutOfMemoryError, as torch's own allocations do."""
+    x = torch.zeros((1 << 19, 1024), dtype=torch.bfloat16, device="cuda")     # 1 GiB
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    fraction = (torch.cuda.memory_reserved() + (1 << 28)) / total
+    torch.cuda.set_per_process_memory_fraction(fraction)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            binding.norm_modulate(x, Norm())
+        with pytest.raises(torch.OutOfMemoryError):
+            binding.gate_residual_norm(x, x, next=Norm())
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert binding.norm_modulate(x[:4], Norm()).shape == (4, 1024)
