@@ -15,6 +15,7 @@
 
 #include <ATen/ops/empty.h>
 
+#include <climits>
 #include <string>
 
 #include "../../include/unstep.h"
@@ -214,6 +215,8 @@ struct Batch {
   int index;
   long long rows, C, groups;  // groups 0: no modulation seen yet
   long long per_group() const { return rows ? rows / (groups ? groups : 1) : 1; }
+  // more than 32 bits hold: a count that the library refuses as it refuses any above its limit
+  int channels() const { return static_cast<int>(C < INT_MAX ? C : INT_MAX - 7); }
 };
 
 struct Vectors {
@@ -317,7 +320,7 @@ PyObject *norm_modulate(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     const Output out = output(a[2], x, at::kBFloat16, "out", at);
     const int status =
         call(lib.norm_modulate, x.data_ptr(), type_code(x), xr.ld, out.t.data_ptr(), out.ld, b.rows,
-             static_cast<int>(b.C), b.per_group(), &spec, at.handle);
+             b.channels(), b.per_group(), &spec, at.handle);
     check(lib, status, "unstep_norm_modulate");
     return out.release();
   });
@@ -357,7 +360,7 @@ PyObject *gate_residual_norm(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         lib.gate_residual_norm, x.data_ptr(), type_code(x), xr.ld, y.data_ptr(), yr.ld, gate.p,
         gate_type, gate.stride, res_scale, is_none(a[4]) ? nullptr : &post, is_none(a[5]) ? nullptr : &next,
         xo.t.data_ptr(), xo.ld, is_none(a[5]) ? nullptr : out.t.data_ptr(), out.ld, b.rows,
-        static_cast<int>(b.C), b.per_group(), at.handle);
+        b.channels(), b.per_group(), at.handle);
     check(lib, status, "unstep_gate_residual_norm");
     PyObject *first = xo.release(), *second = first ? out.release() : nullptr;
     if (!second) {

@@ -54,3 +54,13 @@ def test_views_of_one_buffer(cuda_lib):
         assert e.value.status == binding.UNSTEP_ERR_ARG
     torch.cuda.synchronize()
     assert torch.equal(s, held) and torch.equal(buf, keep)
+
+
+def test_channels_past_32_bits_are_refused(cuda_lib):
+    """2^32 + 64 channels are not 64."""
+    x = torch.zeros((1, 2 ** 32 + 64), dtype=BF, device="cuda")
+    for f in (lambda: binding.norm_modulate(x, Norm(), out=x),
+              lambda: binding.gate_residual_norm(x, x.clone(), next=Norm(), out=torch.empty_like(x))):
+        with pytest.raises(binding.UnstepError) as e:
+            f()
+        assert e.value.status == binding.UNSTEP_ERR_UNSUPPORTED
