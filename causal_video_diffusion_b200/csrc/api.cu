@@ -962,6 +962,7 @@ int unstep_q8_cache_read(const unstep_q8_cache_t *cache, int first_frame, int fr
   p.D = c->D;
   p.rows = static_cast<long long>(c->cap_frames) * c->Hg * c->Wg;
   p.n_rows = frames * c->Hg * c->Wg;
+  p.dev_error = c->dev_error;
   ring_rows(c, first_frame, frames, p.seg_row, p.seg_len);
   if (unstep::launch_q8_cache_read(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) {
     cudaGetLastError();

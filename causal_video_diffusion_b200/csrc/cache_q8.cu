@@ -166,6 +166,10 @@ __global__ void __launch_bounds__(kThreads) q8_cache_read_kernel(const Q8ReadPar
         const int r = static_cast<int>(it / kVecs), c = static_cast<int>(it % kVecs);
         const int row = r < p.seg_len[0] ? p.seg_row[0] + r : p.seg_row[1] + (r - p.seg_len[0]);
         const long long src = (head * p.rows + row) * D + c * 8;
+        if (!debug_check(head >= 0 && head < p.heads && r >= 0 && r < p.n_rows && row >= 0 &&
+                             row < p.rows && c >= 0 && c < kVecs,
+                         p.dev_error))
+          return;
         if (p.k_out) {
           w[k][0] = *reinterpret_cast<const uint2 *>(p.k_cache + src);
           byte[k][0] = p.k_scale[src / kQ8Block];

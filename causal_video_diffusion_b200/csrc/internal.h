@@ -144,6 +144,7 @@ struct Q8ReadParams {
   long long rows;       // cache rows per head
   int n_rows;
   int seg_row[2], seg_len[2];
+  int *dev_error;       // debug build: index checks
 };
 
 cudaError_t launch_q8_cache_read(const Q8ReadParams &p, cudaStream_t stream);

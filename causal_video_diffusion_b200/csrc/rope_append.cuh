@@ -58,10 +58,13 @@ __device__ __forceinline__ bool locate(const RopeAppendParams &p, uint32_t it, I
   if (kDebugChecks) {
     const long long n_act = static_cast<long long>(p.act_B) * p.L * p.act_H * D;
     const long long n_cache = static_cast<long long>(p.B) * p.H * p.rows * D;
+    // from the item's first head to its last
+    const long long more = kHeads > 0 ? (kHeads - 1) * static_cast<long long>(p.H / kHeads) : 0;
     const bool ok = b < static_cast<uint32_t>(p.B) && h < static_cast<uint32_t>(p.H) &&
                     i < static_cast<uint32_t>(p.frames) && y < static_cast<uint32_t>(p.Hg) &&
                     slot >= 0 && slot < p.cap && f >= 0 && f < p.max_pos_t && m.e >= 0 &&
-                    m.e + 8 <= n_act && m.ce >= 0 && m.ce + 8 <= n_cache;
+                    m.e + more * D + 8 <= n_act && m.ce >= 0 &&
+                    m.ce + more * p.rows * D + 8 <= n_cache;
     if (!debug_check(ok, p.dev_error)) return false;
   }
 #pragma unroll

@@ -693,6 +693,15 @@ __global__ void __launch_bounds__((Cfg<D, kRopeQ, kQ8>::kThreads), 1)
       constexpr int kSc = Decoder<D>::kScales;
       TileWalk tw;
       tw.start(p, cta, sk);
+      // debug build: no scales of rows outside the cache
+      auto checked = [&] {
+        if (kDebugChecks && tw.more && !debug_check(tw.sound(p), p.dev_error)) {
+          *abort_flag = 1;
+          tw.more = false;
+          tw.valid = 0;
+        }
+      };
+      checked();
       uint32_t word[2] = {0, 0};
       if (tw.more) {
         word[0] = dec.scales(p.q8.k_scale + tw.first() * kSc, tw.valid);
@@ -703,6 +712,7 @@ __global__ void __launch_bounds__((Cfg<D, kRopeQ, kQ8>::kThreads), 1)
         const int s = n % NS, valid = tw.valid;
         const uint32_t par = (static_cast<uint32_t>(n / NS) & 1u) ^ 1u;
         tw.next(p, cta, sk);
+        checked();
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           ok = __all_sync(kFull, wait_bounded(half ? &empty[s] : &k_empty[s], par, g, E)) &&
