@@ -512,6 +512,15 @@ class LayerCacheQ8(LayerCache):
         return (_HOST or _host()).q8_read(self._at, self._index, first_frame, frames, k_out, v_out,
                                           stream)
 
+    def step_from_host(self, q_h: torch.Tensor, k_h: torch.Tensor, v_h: torch.Tensor,
+                       frame_idx: int, frames: int, window: int, out_h: torch.Tensor,
+                       bufs: dict, stream: Optional[torch.cuda.Stream] = None,
+                       rope_q_in_attn: bool = False) -> torch.Tensor:
+        """LayerCache's, with the queries rotated in the append."""
+        if rope_q_in_attn:      # before anything is copied
+            raise ValueError("an 8-bit cache rotates the queries in the append (no rope_q_in_attn)")
+        return super().step_from_host(q_h, k_h, v_h, frame_idx, frames, window, out_h, bufs, stream)
+
     def state_bytes(self) -> int:
         return lib().unstep_q8_cache_state_bytes(ctypes.byref(self.q8))
 
@@ -535,6 +544,8 @@ class HostStepPipeline:
     """
 
     def __init__(self, cache: LayerCache, device=None, rope_q_in_attn: bool = False):
+        if rope_q_in_attn and isinstance(cache, LayerCacheQ8):
+            raise ValueError("an 8-bit cache rotates the queries in the append (no rope_q_in_attn)")
         c = cache.c
         dev = cache.device if device is None else torch.device(device)
         self.cache = cache

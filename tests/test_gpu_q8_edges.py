@@ -104,3 +104,33 @@ def test_rows_behind_the_last_key(cuda_lib, D, split, Tf):
         assert bool(torch.isnan(cache.window_attn(q, 5)).all())
         assert torch.equal(cache.window_attn(q, window), want), window
     assert cache.device_error() == 0
+
+
+def test_host_steps(cuda_lib):
+    """Steps fed from host memory give the device steps' bits; the query rotation inside the attention,
+    which an 8-bit cache does not have, is refused before anything is copied."""
+    shape = shape_of(1, 2, 64, 4, 6, (24, 20, 20), 2)
+    cache, twin = R.make_cache(shape, 4, 8), R.make_cache(shape, 4, 8)
+    bufs = {n: torch.full((1, 48, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+            for n in ("q", "k", "v", "out")}
+    host = lambda t: t.cpu().pin_memory()  # noqa: E731
+    q, k, v = draw(shape, 5)
+    out = torch.zeros((1, 48, 2, 64), dtype=torch.bfloat16).pin_memory()
+    with pytest.raises(ValueError):
+        binding.HostStepPipeline(cache, rope_q_in_attn=True)
+    for args in ((host(q), host(k), host(v), 0, 2, 2, out, bufs),
+                 (host(q), host(k), host(v), 0, 2, 2, out, bufs, None)):
+        with pytest.raises(ValueError):
+            cache.step_from_host(*args, rope_q_in_attn=True)
+    with pytest.raises(ValueError):
+        cache.step_from_host(*args, True)
+    torch.cuda.synchronize()
+    assert all(bool((t == 7.0).all()) for t in bufs.values()) and cache.frames_written == 0
+    qo = twin.rope_kv_append(q, k, v, 0, 2, q_out=torch.empty_like(q))
+    want = twin.window_attn(qo, 2).cpu()
+    cache.step_from_host(host(q), host(k), host(v), 0, 2, 2, out, bufs)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    out.zero_()
+    binding.HostStepPipeline(cache).run(host(q), host(k), host(v), 0, 2, 2, out, 3)
+    assert torch.equal(out, want) and cache.device_error() == 0
