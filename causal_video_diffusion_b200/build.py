@@ -62,16 +62,21 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
 
 
 def build_host(force: bool = False) -> str:
-    """The extension module of csrc/host_calls.cpp; it reaches the library by addresses alone."""
+    """The extension module of csrc/host_calls.cpp; it reaches the library by addresses alone.  It
+    holds for the torch and the Python that it was compiled against, and carries their names."""
+    import torch
+    made_for = f"host calls for torch {torch.__version__}, {sys.implementation.cache_tag}"
     inputs = [HOST_SOURCE, os.path.join(ROOT, "include", "unstep.h")]
     if not force and os.path.exists(HOST_LIB) and \
             all(os.path.getmtime(f) <= os.path.getmtime(HOST_LIB) for f in inputs):
-        return HOST_LIB
-    import torch
+        with open(HOST_LIB, "rb") as f:
+            if made_for.encode() + b"\0" in f.read():
+                return HOST_LIB
     T = os.path.dirname(torch.__file__)
     tmp = HOST_LIB + f".tmp{os.getpid()}"
     cuda = os.path.dirname(os.path.dirname(NVCC))
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f'-DUNSTEP_MADE_FOR="{made_for}"',
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I" + os.path.join(T, "include"),
            "-I" + os.path.join(T, "include", "torch", "csrc", "api", "include"),

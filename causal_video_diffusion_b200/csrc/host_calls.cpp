@@ -526,7 +526,8 @@ int clear(PyObject *m) {
 }
 
 PyModuleDef_Slot slots[] = {{0, nullptr}};  // multi-phase: a state for every module object
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_host_calls", nullptr, sizeof(Library), methods, slots,
+// the docstring names the torch and Python that this was compiled for; the build looks for it
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_host_calls", UNSTEP_MADE_FOR, sizeof(Library), methods, slots,
                       traverse, clear, nullptr};
 
 }  // namespace

@@ -60,3 +60,31 @@ def test_calls_before_bind_are_refused(host):
         m.bind(RuntimeError)
     with pytest.raises(ValueError):
         m.bind(RuntimeError, 0, 0, 0, 0, 0)
+
+
+def test_another_torch_or_python_rebuilds(host, monkeypatch):
+    """The module built for this torch and Python is kept, and not for others: its next load would
+    meet another ABI."""
+    import subprocess
+    import sys
+    import types
+
+    import torch
+    ran = []
+
+    def run(cmd, **kw):
+        ran.append(cmd)
+        return types.SimpleNamespace(returncode=1, stdout="", stderr="")
+
+    monkeypatch.setattr(subprocess, "run", run)
+    assert cuda_build.build_host() == host and not ran
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", torch.__version__ + ".1")
+        with pytest.raises(RuntimeError):
+            cuda_build.build_host()
+    with monkeypatch.context() as m:
+        m.setattr(sys, "implementation", types.SimpleNamespace(cache_tag="cpython-399"))
+        with pytest.raises(RuntimeError):
+            cuda_build.build_host()
+    assert len(ran) == 2
+    assert torch.__version__ in load(host).__doc__
