@@ -7,12 +7,13 @@
 // pass) and each byte of x, y, x_out and h moves once.  The grid is persistent, a CTA takes
 // consecutive rows, and a row is loaded while the one before it is worked on; what all rows of a
 // group share (weight, bias, modulation, gate) is folded into one factor and one term a channel and
-// stays in registers until the group changes.  What bounds it is HBM for long chunks (30000 gated
-// fp32 rows of 1536 channels: 90 us, 6.1 TB/s; 65536 rows of the norm alone: 84 us, 4.8 TB/s), and
-// the chain of loads and two sums a row, which only many resident CTAs hide, for ordinary ones
-// (4680 rows of 1536: 18.7 us gated, 10.4 us the norm).  Measured instead for the gated 4680 rows:
-// parameters read for every row 22 us, two vectors a thread 22-24, a row a warp 29, two to four rows
-// loaded ahead 25-28 (fewer CTAs fit).  Above 8192 channels the parameters spill (2 TB/s).
+// stays in registers until the group changes.  What bounds it is HBM for long gated chunks (30000
+// fp32 rows of 1536 channels: 89 us, 6.2 TB/s), and the chain of loads and two sums a row, which only
+// many resident CTAs hide, for the norm alone (65536 rows of 1536: 81 us, 5.0 TB/s) and for ordinary
+// chunks (4680 rows of 1536, call after call: 16.9 us gated, 7.9 us the norm).  Measured instead for
+// the gated 4680 rows, 18.7 us before launches overlapped: parameters read for every row 22 us, two
+// vectors a thread 22-24, a row a warp 29, two to four rows loaded ahead 25-28 (fewer CTAs fit).  Above
+// 8192 channels the gated form's parameters spill (1.7 to 2.2 TB/s).
 #include <cuda_bf16.h>
 
 #include "block_norm.h"
@@ -373,6 +374,16 @@ cudaError_t launch_block_norm(const NormParams &in, bool gated, cudaStream_t s) 
   if (p.has_post) add_norm(p.post);
   add_norm(p.next);
   p.wide = (low & 31) == 0;
+  // The narrowest place that holds a row's vectors: lanes of a warp, then warps, one vector a
+  // thread as long as that keeps several CTAs on an SM, more above.  Threads behind the row's end
+  // only pass the barriers, so a step too wide costs its share of the resident rows.  TB/s of the
+  // norm of bf16 rows and of gated fp32 rows (46 million elements), with the step and with the next
+  // one above in its place: 128 channels 4.98 and 6.04 against 3.01 and 4.79; 512: 4.89 and 6.16,
+  // 2.65 and 4.89; 1536: 4.64 and 6.23, 3.61 and 5.65; 1280, inside that step: 3.94 and 5.86, 3.10
+  // and 5.20.  One vector or two a thread: 4096 channels 5.02 and 6.01 with two in 8 warps, 3.98
+  // and 5.30 with one in 16; 2048: 4.44 and 6.23 with one in 8, 5.12 and 5.94 with two in 4.  Two
+  // or four: 8192 channels 4.10 and 5.92 with two in 16, 3.78 and 5.48 with four in 8.  Widths that
+  // lie badly: 2560 runs at 4.11 and 5.49, 5120 at 3.22 and 5.36, 6144 at 3.60 and 5.81.
   if (p.C <= 64) return launch<8, 1, 1>(p, gated, s);
   if (p.C <= 128) return launch<16, 1, 1>(p, gated, s);
   if (p.C <= 256) return launch<32, 1, 1>(p, gated, s);

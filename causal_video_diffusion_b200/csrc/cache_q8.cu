@@ -5,9 +5,10 @@
 // the v quantised in registers: the four lanes that hold a 32-channel block share its maximum by
 // two shuffles, then every lane writes the eight codes of its vector.  It moves 10 + 1/16 bytes
 // for every element of the chunk (q read and written, k and v read in bf16, two codes and their
-// share of two scale bytes) where the bf16 append moves 12.  Measured: 12.3 us for 4680 tokens of 12
-// heads of 128 (5.9 TB/s), four such streams 48.4 us (6.0 TB/s).
-// Read-back: 6 + 1/16 bytes an element of K and V: 7.4 and 29.4 us, 5.9 TB/s, at the same sizes.
+// share of two scale bytes) where the bf16 append moves 12.  Measured, call after call on three sets of
+// inputs: 13.1 us for 4680 tokens of 12 heads of 128 (5.5 TB/s), four such streams 47.6 us (6.1 TB/s).
+// Read-back: 6 + 1/16 bytes an element of K and V: 6.4 us for that chunk (its codes in L2), 28.4 us
+// for the four (6.1 TB/s).
 #include <cuda_bf16.h>
 
 #include "internal.h"

@@ -34,7 +34,10 @@
 // tile's codes into shared memory as they lie in the cache; warps 12-15 decode them (about 2.3
 // instructions an element), write the tile as bf16 into the stage that the TMA would have filled,
 // and announce it; rows behind the segment's end become zeros.  Everything behind the stage is the
-// bf16 kernel's.
+// bf16 kernel's, its rounding of P to bf16 for the second product too: one product takes both operands
+// in one type, and the stored V has bf16's range, not fp16's.  It costs 2^-8 relative in each
+// probability (the sum takes them unrounded): 0.0024 RMS of the output against 64 bits, where the
+// output's own rounding alone gives 0.0017.
 //
 // Every wait is bounded (WaitGuard): on a timeout the CTA records UNSTEP_ERR_DEVICE_TIMEOUT,
 // lets in-flight TMA copies and MMAs land, frees TMEM and exits.
